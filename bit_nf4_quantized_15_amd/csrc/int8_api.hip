@@ -1,0 +1,215 @@
+// C ABI of the int8 layer: argument validation and dispatch (declared in include/qlora.h,
+// section "int8").
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <new>
+#include <vector>
+
+#include "int8.h"
+#include "lora_plan.h"
+
+using namespace qlora;
+
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
+inline int dt_of(int dtype) { return dtype == QLORA_DTYPE_F16 ? kDtF16 : kDtBf16; }
+inline bool is16(int dtype) { return dtype == QLORA_DTYPE_BF16 || dtype == QLORA_DTYPE_F16; }
+
+// A weight (min_rows 1) or activations (min_rows 0, where an empty one needs no pointers).
+qlora_status check_int8(const qlora_int8* q, int64_t min_rows) {
+    if (!q || q->rows < min_rows || q->cols < 1 || !is16(q->dtype)) return QLORA_ERR_INVALID_ARG;
+    if (q->cols % kBlock || q->rows > INT32_MAX || q->cols > INT32_MAX) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (q->rows == 0) return QLORA_OK;
+    if (!q->codes || !q->scale) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(q->codes) || !aligned16(q->scale)) return QLORA_ERR_MISALIGNED;
+    return QLORA_OK;
+}
+
+inline bool bad_rank(int r) { return r < 0 || r > 128; }
+inline bool bad_m(int64_t M) { return M < 0 || M > INT32_MAX; }
+inline bool bad_sizes(int64_t M, int64_t N, int64_t K, int r) {
+    return bad_m(M) || N < 1 || K < 1 || N > INT32_MAX || K > INT32_MAX || bad_rank(r);
+}
+
+struct FwdWs {
+    size_t codes, scale, tbuf, part, total;  // x in 8 bits; t when the caller keeps none; split sums of t
+};
+inline FwdWs fwd_ws(int64_t M, int64_t K, int r) {
+    FwdWs w{};
+    w.codes = 0;
+    w.scale = align256((size_t)M * K);
+    w.tbuf = w.scale + align256((size_t)M * 4);
+    w.part = w.tbuf + align256((size_t)M * r * 2);
+    w.total = w.part + (r ? align256(nt_ws_bytes(M, K, r)) : 0);
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+qlora_status qlora_int8_quantize(const uint16_t* x, const qlora_int8* out, void* stream) {
+    const qlora_status st = check_int8(out, 0);
+    if (st != QLORA_OK) return st;
+    if (out->rows == 0) return QLORA_OK;
+    if (!x) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(x)) return QLORA_ERR_MISALIGNED;
+    return launch_int8_quantize(x, out->rows, out->cols, out->codes, out->scale, dt_of(out->dtype),
+                                (hipStream_t)stream);
+}
+
+qlora_status qlora_int8_dequantize(const qlora_int8* q, uint16_t* out, void* stream) {
+    const qlora_status st = check_int8(q, 0);
+    if (st != QLORA_OK) return st;
+    if (q->rows == 0) return QLORA_OK;
+    if (!out) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(out)) return QLORA_ERR_MISALIGNED;
+    return launch_int8_dequantize(q->codes, q->scale, q->rows, q->cols, dt_of(q->dtype), out, (hipStream_t)stream);
+}
+
+size_t qlora_int8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r) {
+    if (bad_sizes(M, N, K, r) || M == 0 || K % kBlock) return 0;
+    return fwd_ws(M, K, r).total;
+}
+
+qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                                   const uint16_t* B, int r, float alpha, uint16_t* y, uint16_t* t_out,
+                                   const qlora_int8* x_keep, void* ws, size_t ws_bytes, void* stream) {
+    qlora_status st = check_int8(w, 1);
+    if (st != QLORA_OK) return st;
+    const int64_t N = w->rows, K = w->cols;
+    if (bad_m(M) || bad_rank(r) || (r && !std::isfinite(alpha))) return QLORA_ERR_INVALID_ARG;
+    if (K >= kInt8MaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (x_keep) {
+        if ((st = check_int8(x_keep, 0)) != QLORA_OK) return st;
+        if (x_keep->rows != M || x_keep->cols != K || x_keep->dtype != w->dtype) return QLORA_ERR_INVALID_ARG;
+    }
+    if (M == 0) return QLORA_OK;
+    if (!x || !y || (r && (!A || !B)) || (!r && (A || B || t_out))) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(A) || !aligned16(B) || !aligned16(t_out))
+        return QLORA_ERR_MISALIGNED;
+    const FwdWs W = fwd_ws(M, K, r);
+    if (!ws || ws_bytes < W.total) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QLORA_ERR_MISALIGNED;
+    hipStream_t s = (hipStream_t)stream;
+    const int dt = dt_of(w->dtype);
+    int8_t* xq = x_keep ? x_keep->codes : reinterpret_cast<int8_t*>(at(ws, W.codes));
+    float* sx = x_keep ? x_keep->scale : reinterpret_cast<float*>(at(ws, W.scale));
+    uint16_t* t = t_out ? t_out : reinterpret_cast<uint16_t*>(at(ws, W.tbuf));
+    if ((st = launch_int8_quantize(x, M, K, xq, sx, dt, s)) != QLORA_OK) return st;
+    if (r && (st = launch_nt(x, A, true, at(ws, W.part), t, alpha / (float)r, (int)M, (int)K, r, dt, s)) != QLORA_OK)
+        return st;
+    return launch_int8_gemm_fwd(xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, dt, s);
+}
+
+qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const uint16_t* t, const uint16_t* B,
+                                 int r, uint16_t* y, void* stream) {
+    qlora_status st = check_int8(w, 1);
+    if (st != QLORA_OK || (st = check_int8(x, 0)) != QLORA_OK) return st;
+    if (x->cols != w->cols || x->dtype != w->dtype || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
+    if (w->cols >= kInt8MaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (x->rows == 0) return QLORA_OK;
+    if (!y || (r && (!t || !B)) || (!r && (t || B))) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned16(t) || !aligned16(B)) return QLORA_ERR_MISALIGNED;
+    return launch_int8_gemm_fwd(x->codes, x->scale, w->codes, w->scale, t, B, y, (int)x->rows, (int)w->rows,
+                                (int)w->cols, r, dt_of(w->dtype), (hipStream_t)stream);
+}
+
+size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r) {
+    if (bad_sizes(M, N, K, r) || M == 0 || r == 0) return 0;
+    return align256(nt_ws_bytes(M, N, r));
+}
+
+qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                      float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    qlora_status st = check_int8(w, 1);
+    if (st != QLORA_OK) return st;
+    const int64_t N = w->rows, K = w->cols;
+    if (bad_m(M) || bad_rank(r) || (r && !std::isfinite(alpha))) return QLORA_ERR_INVALID_ARG;
+    if (M == 0) return QLORA_OK;
+    if (!dy || !dx || (r && (!A || !B || !u)) || (!r && (A || B || u))) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(dy) || !aligned16(u) || !aligned16(dx))
+        return QLORA_ERR_MISALIGNED;
+    const size_t need = qlora_int8_linear_bwd_dx_workspace(M, N, K, r);
+    if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+    if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
+    hipStream_t s = (hipStream_t)stream;
+    const int dt = dt_of(w->dtype);
+    if (r && (st = launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt, s)) != QLORA_OK) return st;
+    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt, s);
+}
+
+qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                    const uint16_t* A, int r, uint16_t* dx, void* stream) {
+    const qlora_status st = check_int8(w, 1);
+    if (st != QLORA_OK) return st;
+    if (bad_m(M) || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
+    if (M == 0) return QLORA_OK;
+    if (!dy || !dx || (r && (!u || !A)) || (!r && (u || A))) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(dx) || !aligned16(u) || !aligned16(A)) return QLORA_ERR_MISALIGNED;
+    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)w->rows, (int)w->cols, r,
+                                   dt_of(w->dtype), (hipStream_t)stream);
+}
+
+// One layer of qlora_lora_grads_batch_int8: x restored, then the two contractions.
+static size_t grads_layer_ws(const qlora_lora_grads_int8& g, int r) {
+    if (g.M == 0) return 0;
+    return align256((size_t)g.M * g.K * 2) + align256(tn_ws_bytes(g.M, g.K, r)) + align256(tn_ws_bytes(g.M, g.N, r));
+}
+
+size_t qlora_lora_grads_batch_int8_workspace(const qlora_lora_grads_int8* layers, int count, int r) {
+    if (!layers || count <= 0 || r < 1 || r > 128) return 0;
+    size_t total = 0;
+    for (int i = 0; i < count; ++i)
+        if (!bad_sizes(layers[i].M, layers[i].N, layers[i].K, r)) total += grads_layer_ws(layers[i], r);
+    return total;
+}
+
+qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, int count, int r, int dtype, void* ws,
+                                         size_t ws_bytes, void* stream) {
+    if (count < 0 || r < 1 || r > 128 || !is16(dtype)) return QLORA_ERR_INVALID_ARG;
+    if (count == 0) return QLORA_OK;
+    if (!layers) return QLORA_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {  // every entry is checked before anything is launched
+        const qlora_lora_grads_int8& g = layers[i];
+        if (bad_sizes(g.M, g.N, g.K, r) || !g.dA || !g.dB) return QLORA_ERR_INVALID_ARG;
+        if (g.K % kBlock) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        if (!aligned16(g.dA) || !aligned16(g.dB)) return QLORA_ERR_MISALIGNED;
+        if (g.M == 0) continue;
+        if (!g.x || !g.x_scale || !g.t || !g.u || !g.dy) return QLORA_ERR_INVALID_ARG;
+        if (!aligned16(g.x) || !aligned16(g.x_scale) || !aligned16(g.t) || !aligned16(g.u) || !aligned16(g.dy))
+            return QLORA_ERR_MISALIGNED;
+    }
+    const size_t need = qlora_lora_grads_batch_int8_workspace(layers, count, r);
+    if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+    if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
+    hipStream_t s = (hipStream_t)stream;
+    const int dt = dt_of(dtype);
+    size_t off = 0;
+    for (int i = 0; i < count; ++i) {
+        const qlora_lora_grads_int8& g = layers[i];
+        qlora_status st;
+        if (g.M == 0) {  // empty sums
+            if ((st = launch_fill(g.dA, g.K * r, 0.0f, s)) != QLORA_OK) return st;
+            if ((st = launch_fill(g.dB, (int64_t)r * g.N, 0.0f, s)) != QLORA_OK) return st;
+            continue;
+        }
+        uint16_t* x16 = reinterpret_cast<uint16_t*>(at(ws, off));
+        off += align256((size_t)g.M * g.K * 2);
+        if ((st = launch_int8_dequantize(g.x, g.x_scale, g.M, g.K, dt, x16, s)) != QLORA_OK) return st;
+        TnDesc d[2];
+        d[0] = TnDesc{x16, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1};
+        off += align256(tn_ws_bytes(g.M, g.K, r));
+        d[1] = TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N};
+        off += align256(tn_ws_bytes(g.M, g.N, r));
+        if ((st = launch_tn_batch(d, 2, r, dt, s)) != QLORA_OK) return st;
+    }
+    return QLORA_OK;
+}
+
+}  // extern "C"

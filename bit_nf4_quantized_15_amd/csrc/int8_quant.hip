@@ -1,0 +1,155 @@
+// int8 codes with one fp32 scale per row, and the 16-bit values back from them
+// ("bitsandbytes deep dive", section 4: absmax int8, one scale per row).
+//
+// With a = max|x| of the row, the code is the integer nearest to 127 x / a in exact
+// arithmetic, ties toward zero.  One fma decides it: fma(x, inv, 1.5 * 2^23) with
+// inv = fl(127/a) (1 - 2^-21), whose low byte is the rounded integer in two's
+// complement.  inv is below 127/a by a relative 2^-21 +- 2^-23.  A real quotient that is
+// no tie lies at least 1/(254 * 2047) > 2^-19 (fp16; bf16 1/(254 * 255) > 2^-16) of itself
+// away from any half-integer, because 254 x and (2j + 1) a differ by a whole unit of
+// x's mantissa; so the small cut moves no such quotient across a half, and it moves every
+// tie to just below its half: toward zero.
+#include "int8.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kQT = 256;   // lanes per row
+
+template <int DT>
+constexpr uint32_t kInfBits = DT == kDtF16 ? 0x7C00u : 0x7F80u;
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// The larger magnitude bits of two packed pairs (as integers: NaN above infinity above finite).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
+    const u16x2_t a = __builtin_bit_cast(u16x2_t, m), b = __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+}
+
+// What a row's codes need: one multiplier (and a power of two for rows of tiny values,
+// whose reciprocal would overflow).
+struct RowScale {
+    float inv, pre, scale;
+    bool bad;
+};
+template <int DT>
+__device__ __forceinline__ RowScale row_scale(uint32_t abits) {
+    RowScale r;
+    r.bad = abits >= kInfBits<DT>;
+    const float a = h16_to_f32<DT>(abits);
+    r.scale = r.bad ? __builtin_nanf("") : a / 127.0f;
+    r.pre = DT == kDtBf16 && a < 0x1p-100f ? 0x1p100f : 1.0f;   // exact: bf16 values are multiples of 2^-133
+    r.inv = abits == 0u || r.bad ? 0.0f : 127.0f / (a * r.pre) * (1.0f - 0x1p-21f);
+    return r;
+}
+
+// Codes of the 8 values of v; zero rows and rows that are not finite give 0 (inv = 0, and
+// for the latter the value is replaced before the fma).
+template <int DT>
+__device__ __forceinline__ u32x2_t codes8(u32x4_t v, const RowScale& r) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = r.bad ? 0u : v[i];
+        float lo = h16_to_f32<DT>(w & 0xFFFFu), hi = h16_to_f32<DT>(w >> 16);
+        if (DT == kDtBf16) {
+            lo *= r.pre;
+            hi *= r.pre;
+        }
+        b[2 * i] = __float_as_uint(__builtin_fmaf(lo, r.inv, 12582912.0f));
+        b[2 * i + 1] = __float_as_uint(__builtin_fmaf(hi, r.inv, 12582912.0f));
+    }
+    u32x2_t o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t p01 = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0400u);
+        const uint32_t p23 = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000C0Cu);
+        o[i] = p01 | p23;
+    }
+    return o;
+}
+
+// One workgroup per row, two passes over it.
+template <int DT>
+__global__ __launch_bounds__(kQT) void int8_quantize_kernel(const uint16_t* __restrict__ x, int cols,
+                                                            int8_t* __restrict__ codes, float* __restrict__ scale) {
+    __shared__ uint32_t red[kQT / 64];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + row * cols);
+    u32x2_t* cr = reinterpret_cast<u32x2_t*>(codes + row * cols);
+    const int nch = cols >> 3;
+    uint32_t m = 0;
+    for (int c = tid; c < nch; c += kQT) {
+        const u32x4_t v = xr[c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_abs2(m, v[i]);
+    }
+    uint32_t a = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, d));
+    if ((tid & 63) == 0) red[tid >> 6] = a;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQT / 64; ++w) a = max(a, red[w]);
+    const RowScale r = row_scale<DT>(a);
+    if (tid == 0) scale[row] = r.scale;
+    for (int c = tid; c < nch; c += kQT) cr[c] = codes8<DT>(xr[c], r);
+}
+
+// 16 codes per lane; `base` counts 16-code chunks of the whole tensor.
+constexpr int kDqPer = 1024;  // chunks per workgroup
+template <int DT>
+__global__ __launch_bounds__(256) void int8_dequantize_kernel(const int8_t* __restrict__ codes,
+                                                              const float* __restrict__ scale, int64_t rows, int cols,
+                                                              uint16_t* __restrict__ out) {
+    const uint32_t cpr = (uint32_t)cols >> 4;
+    const int64_t base = (int64_t)blockIdx.x * kDqPer;
+    const int64_t row0 = base / cpr;
+    const uint32_t rem = (uint32_t)(base - row0 * cpr);
+#pragma unroll
+    for (int e = 0; e < kDqPer / 256; ++e) {
+        const uint32_t i = rem + (uint32_t)(threadIdx.x + 256 * e);
+        const int64_t row = row0 + i / cpr;
+        if (row >= rows) continue;
+        const int64_t chunk = base + threadIdx.x + 256 * e;
+        const u32x4_t c = reinterpret_cast<const u32x4_t*>(codes)[chunk];
+        const float s = scale[row];
+        u32x4_t o[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u32x2_t v = int8_values4<DT>(c[j], s);
+            o[j >> 1][2 * (j & 1)] = v[0];
+            o[j >> 1][2 * (j & 1) + 1] = v[1];
+        }
+        u32x4_t* dst = reinterpret_cast<u32x4_t*>(out) + 2 * chunk;
+        dst[0] = o[0];
+        dst[1] = o[1];
+    }
+}
+
+}  // namespace
+
+qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scale, int dt,
+                                  hipStream_t s) {
+    with_dt(dt, [&](auto dtc) {
+        constexpr int DT = decltype(dtc)::value;
+        hipLaunchKernelGGL(int8_quantize_kernel<DT>, dim3((unsigned)rows), dim3(kQT), 0, s, x, (int)cols, codes, scale);
+    });
+    return launch_status();
+}
+
+qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int dt,
+                                    uint16_t* out, hipStream_t s) {
+    const int64_t wgs = (rows * (cols >> 4) + kDqPer - 1) / kDqPer;
+    if (wgs >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    with_dt(dt, [&](auto dtc) {
+        constexpr int DT = decltype(dtc)::value;
+        hipLaunchKernelGGL(int8_dequantize_kernel<DT>, dim3((unsigned)wgs), dim3(256), 0, s, codes, scale, rows,
+                           (int)cols, out);
+    });
+    return launch_status();
+}
+
+}  // namespace qlora

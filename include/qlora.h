@@ -373,6 +373,93 @@ qlora_status qlora_pooled_bwd(const qlora_nf4* w, const uint16_t* x, int64_t M, 
                               const uint16_t* dy, uint16_t* dx, float* dA, float* dB, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* ---- int8: an 8-bit frozen base, and activations kept in 8 bits -------------
+ * (deep dive, section 4: absmax int8, and vector-wise int8 with a scale for each
+ * row of x and each output of W.)  One format serves both.  Of a [rows, cols] tensor it holds
+ * int8 codes and one fp32 scale per row:
+ *   a = max |x| over the row,   scale = fl32(a / 127),
+ *   code = the integer nearest to 127 x / a in exact arithmetic, ties toward
+ *          zero (so in -127 .. 127);  a = 0 gives scale 0 and codes 0.
+ * A code stands for RNE_16( fl32( scale * code ) ) in the compute dtype (bf16 or
+ * fp16; there is no fp32 form).  A weight W [N, K] has a scale per output n, x
+ * [M, K] one per token m.  Here inputs need not be finite: a row that holds an
+ * infinity or a NaN gets scale NaN and codes 0, so its outputs are NaN and other
+ * rows are untouched. */
+typedef struct qlora_int8 {
+    int8_t* codes;  /* [rows, cols] row-major                                   */
+    float* scale;   /* [rows]                                                   */
+    int64_t rows;   /* N of a weight, M of activations                          */
+    int64_t cols;   /* K, a multiple of 64                                      */
+    int32_t dtype;  /* a qlora_dtype, bf16 or fp16: the 16-bit format of the    */
+                    /* tensors it is used with; any other -> INVALID_ARG        */
+} qlora_int8;
+
+/* Quantize x [rows, cols] (bf16 or fp16 by out->dtype) into out: a weight, or
+ * activations to be kept for the backward.  rows == 0 is a no-op.
+ * Errors: null pointer, rows < 0, cols < 1 or another dtype -> INVALID_ARG;
+ * cols % 64 or a size of 2^31 or more -> UNSUPPORTED_SHAPE; alignment ->
+ * MISALIGNED (codes, scale and x 16 bytes). */
+qlora_status qlora_int8_quantize(const uint16_t* x, const qlora_int8* out, void* stream);
+
+/* The 16-bit values that the codes stand for, into out [rows, cols]: restores an
+ * activation checkpoint, exports a weight.  Errors as qlora_int8_quantize. */
+qlora_status qlora_int8_dequantize(const qlora_int8* q, uint16_t* out, void* stream);
+
+/* Forward of the int8 linear layer with its LoRA branch:
+ *   (xq, sx) = quantize(x)
+ *   t = s * (x A)                                     [M, r], s = alpha / r
+ *   y[m, n] = RNE_16( sx[m] sw[n] sum_k xq[m,k] wq[n,k] + sum_j t[m,j] B[j,n] )
+ * The int8 sum is exact (int32; K < 131072), everything after it is fp32 up to
+ * the one rounding of y; t is the 16-bit t that qlora_lora_down defines.
+ * x_keep (nullable) receives (xq, sx), rows == M, cols == K and the weight's
+ * dtype: the activation checkpoint that qlora_lora_grads_batch_int8 takes later,
+ * after which x itself can be freed.  r == 0: no LoRA branch (A, B and t_out
+ * NULL; alpha is not used), 1 <= r <= 128 otherwise; t_out is nullable.
+ * qlora_int8_gemm_fwd is the product for a given (xq, sx) and t (t, B NULL when
+ * r == 0), with no workspace.  M == 0 is a no-op.  Errors as qlora_linear_fwd,
+ * plus K >= 131072 -> UNSUPPORTED_SHAPE. */
+size_t qlora_int8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r);
+qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                                   const uint16_t* B, int r, float alpha, uint16_t* y, uint16_t* t_out,
+                                   const qlora_int8* x_keep, void* ws, size_t ws_bytes, void* stream);
+qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const uint16_t* t, const uint16_t* B,
+                                 int r, uint16_t* y, void* stream);
+
+/* Input gradient of the int8 layer (the base is frozen: no dW), on the 16-bit
+ * values of the weight as everywhere in this library:
+ *   u  = s * (dy B^T)            [M, r]  into the caller's u (kept for the gradients)
+ *   dx = dy W_16 + u A^T         [M, K],  W_16[n, k] = RNE_16( fl32( sw[n] * wq[n, k] ) )
+ * r == 0: dx = dy W_16 (A, B, u NULL, no workspace).  qlora_int8_gemm_bwd_dx is
+ * the dx stage for a given u.  M == 0 is a no-op.  Errors as qlora_linear_bwd_dx. */
+size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
+qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                      float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
+                                      size_t ws_bytes, void* stream);
+qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                    const uint16_t* A, int r, uint16_t* dx, void* stream);
+
+/* qlora_lora_grads_batch with each layer's x given as its 8-bit checkpoint (of
+ * NF4, FP4 and int8 layers alike):
+ *   dA = x_16^T u   [K, r] fp32,   dB = t^T dy   [r, N] fp32 (overwritten),
+ * x_16[m, k] = RNE_16( fl32( x_scale[m] * x[m, k] ) ), the tensor that
+ * qlora_int8_dequantize restores; it is formed in registers, never in memory.
+ * dtype is the format of t, u, dy and x_16.  Deterministic.  Arguments, empty
+ * layers and errors as qlora_lora_grads_batch, plus K % 64 -> UNSUPPORTED_SHAPE. */
+typedef struct qlora_lora_grads_int8 {
+    const int8_t* x;      /* [M, K] codes of the layer's input             */
+    const float* x_scale; /* [M]                                           */
+    const uint16_t* t;    /* [M, r] the forward's t                        */
+    const uint16_t* u;    /* [M, r] u = s dy B^T                           */
+    const uint16_t* dy;   /* [M, N] the upstream gradient                  */
+    float* dA;            /* [K, r] fp32 out                               */
+    float* dB;            /* [r, N] fp32 out                               */
+    int64_t M, N, K;
+} qlora_lora_grads_int8;
+
+size_t qlora_lora_grads_batch_int8_workspace(const qlora_lora_grads_int8* layers, int count, int r);
+qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, int count, int r, int dtype, void* ws,
+                                         size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,389 @@
+"""The int8 operators on the GPU against float64 (oracle/int8.py).
+
+Codes, scales and restored values are compared bit for bit.  Products are compared element
+by element with bounds that come from the arithmetic: h = eps / 2 of the 16-bit type for
+each rounding to it (of the output, and of t or u where the formula goes through them; half
+the smallest subnormal more for fp16), and for fp32 sums of n products, in whatever order,
+(n + 8) 2^-23 of the sum of their magnitudes.  Outputs start as NaN (tests/conftest.py).
+"""
+import numpy as np
+import pytest
+
+from bit_nf4_quantized_15_amd import workloads
+from oracle import bf16, f16, int8
+
+from gpu_util import dev_bf16, dev_f16, host_bits, say
+
+pytestmark = pytest.mark.gpu
+
+FMT = {"bf16": (bf16, dev_bf16, 2.0 ** -8, 0.0), "f16": (f16, dev_f16, 2.0 ** -11, 2.0 ** -25)}
+
+
+@pytest.fixture(scope="module")
+def q():
+    from bit_nf4_quantized_15_amd import qlora
+    return qlora
+
+
+def bits(fmt, seed, shape, std=1.0):
+    return (workloads.normal_bf16 if fmt == "bf16" else workloads.normal_f16)(seed, shape, std)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def close(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
+                          f"{got[bad][0]} for {want[bad][0]}, tolerance {np.broadcast_to(tol, got.shape)[bad][0]}"
+
+
+class Layer:
+    """One layer's inputs on both sides, and what the oracle says of it."""
+
+    def __init__(self, q, fmt, seed, M, N, K, r, alpha=16.0):
+        self.m, self.dev, self.h, self.sub = FMT[fmt]
+        self.fmt, self.M, self.N, self.K, self.r, self.alpha = fmt, M, N, K, r, alpha
+        self.s = alpha / r if r else 0.0
+        self.xb, self.wb = bits(fmt, seed, (M, K)), bits(fmt, seed + 1, (N, K), 0.02)
+        self.dyb = bits(fmt, seed + 4, (M, N), 0.5)
+        if M >= 3:
+            self.xb[1] = 0                                       # a padded token
+        self.cx, self.sx = int8.quantize(self.xb, fmt)
+        self.cw, self.sw = int8.quantize(self.wb, fmt)
+        self.x, self.dy = self.dev(self.xb), self.dev(self.dyb)
+        self.w = q.int8_quantize(self.dev(self.wb))
+        to = self.m.to_f64
+        self.xf, self.dyf = to(self.xb), to(self.dyb)
+        self.x16, self.w16 = (to(int8.dequantize(c, s, fmt)) for c, s in ((self.cx, self.sx), (self.cw, self.sw)))
+        self.A = self.B = self.Af = self.Bf = None
+        if r:
+            Ab, Bb = bits(fmt, seed + 2, (K, r), r ** -0.5), bits(fmt, seed + 3, (r, N), 0.05)
+            self.A, self.B, self.Af, self.Bf = self.dev(Ab), self.dev(Bb), to(Ab), to(Bb)
+
+    def check_t(self, t):
+        want = self.s * (self.xf @ self.Af)
+        tol = self.h * np.abs(want) + self.sub + (self.K + 8) * 2.0 ** -23 * self.s * (np.abs(self.xf) @ np.abs(self.Af))
+        close(f64(t), want, tol * (1 + self.h), "t")
+        return tol
+
+    def check_y(self, y, t=None):
+        """t given: y against that very t."""
+        base, _ = int8.linear_fwd(self.xf, self.cx, self.sx, self.cw, self.sw)
+        want, mag, tol = base, np.abs(base), 0.0
+        if self.r:
+            tt = self.s * (self.xf @ self.Af) if t is None else f64(t)
+            if t is None:
+                tol = (self.h * np.abs(tt) + self.sub + (self.K + 8) * 2.0 ** -23 * self.s *
+                       (np.abs(self.xf) @ np.abs(self.Af))) @ np.abs(self.Bf)
+            want, mag = base + tt @ self.Bf, mag + np.abs(tt) @ np.abs(self.Bf)
+        tol = tol + (self.r + 8) * 2.0 ** -23 * mag
+        close(f64(y), want, (tol + self.h * np.abs(want) + self.sub) * (1 + 2 * self.h), "y")
+
+    def check_u(self, u):
+        want = self.s * (self.dyf @ self.Bf.T)
+        tol = self.h * np.abs(want) + self.sub + (self.N + 8) * 2.0 ** -23 * self.s * (np.abs(self.dyf) @ np.abs(self.Bf.T))
+        close(f64(u), want, tol * (1 + self.h), "u")
+
+    def check_dx(self, dx, u):
+        want, mag = self.dyf @ self.w16, np.abs(self.dyf) @ np.abs(self.w16)
+        if self.r:
+            want, mag = want + f64(u) @ self.Af.T, mag + np.abs(f64(u)) @ np.abs(self.Af.T)
+        tol = (self.N + self.r + 8) * 2.0 ** -23 * mag
+        close(f64(dx), want, (tol + self.h * np.abs(want) + self.sub) * (1 + 2 * self.h), "dx")
+
+    def check_grads(self, dA, dB, t, u):
+        for name, g, X, S in (("dA", dA, self.x16, f64(u)), ("dB", dB, f64(t), self.dyf)):
+            close(f64(g), X.T @ S, (self.M + 8) * 2.0 ** -23 * (np.abs(X).T @ np.abs(S)) + 2.0 ** -149, name)
+
+
+# ---- codes
+ROWS = [("bf16", 1, 64), ("f16", 3, 64), ("bf16", 5, 128), ("bf16", 70, 320), ("f16", 9, 2048), ("bf16", 4, 4096),
+        ("f16", 2, 8192), ("bf16", 3, 11008), ("bf16", 2, 28672), ("f16", 2, 32768 + 64), ("bf16", 600, 192),
+        ("bf16", 130, 4160)]
+
+
+@pytest.mark.parametrize("fmt,rows,cols", ROWS)
+def test_codes_scales_and_values_are_exact(q, fmt, rows, cols):
+    m, dev, _, _ = FMT[fmt]
+    say(f"[int8 codes] {fmt} {rows}x{cols}")
+    b = bits(fmt, 100 + rows + cols, (rows, cols))
+    if rows > 1:
+        b[1] = 0
+        b[0, ::3] &= 0x8000                                        # both zeros
+    if rows > 2:
+        b[2] = m.from_f32_rne(np.arange(cols, dtype=np.float32) % 254 + 0.0)
+        b[2, 0] = m.from_f32_rne(np.float32(254.0))                # odd values are ties
+    x = dev(b)
+    t = q.int8_quantize(x)
+    back = q.int8_dequantize(t)
+    codes, scale = int8.quantize(b, fmt)
+    assert np.array_equal(t.codes.cpu().numpy(), codes)
+    assert np.array_equal(t.scale.cpu().numpy(), scale)
+    assert np.array_equal(host_bits(back), int8.dequantize(codes, scale, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+def test_codes_over_the_formats_range(q, fmt):
+    """Rows whose largest value is a subnormal, a tiny or the largest value of the format, random patterns."""
+    say(f"[int8 codes] {fmt} extreme rows")
+    m, dev, _, _ = FMT[fmt]
+    top = 0x7F7F if fmt == "bf16" else 0x7BFF
+    g = np.random.default_rng(2)
+    tops = [1, 2, 3, 0x7F, 0x80, 0x100, 0x0D00, 0x0E80, top - 1, top] + list(g.integers(1, top, 54))
+    b = np.stack([g.integers(max(0, a - 1500), a + 1, 512) for a in tops]).astype(np.uint16)
+    b[:, 5] = tops
+    b |= (g.integers(0, 2, b.shape) << 15).astype(np.uint16)
+    t = q.int8_quantize(dev(b))
+    codes, scale = int8.quantize(b, fmt)
+    assert np.array_equal(t.codes.cpu().numpy(), codes)
+    assert np.array_equal(t.scale.cpu().numpy(), scale)
+    assert np.array_equal(host_bits(q.int8_dequantize(t)), int8.dequantize(codes, scale, fmt))
+
+
+def test_rows_that_are_not_finite_stay_alone(q):
+    """A row with an infinity or a NaN: scale NaN, codes 0, its y NaN; the other rows are what they are without it."""
+    import torch
+    say("[int8] rows that are not finite")
+    M, N, K = 21, 72, 192
+    L = Layer(q, "bf16", 900, M, N, K, 0)
+    y0, _ = q.int8_linear_fwd(L.w, L.x)
+    x = L.x.clone()
+    x[4, 7], x[9, 0], x[9, 100], x[20, 191] = float("inf"), float("nan"), float("-inf"), float("nan")
+    t = q.int8_quantize(x)
+    y, _ = q.int8_linear_fwd(L.w, x)
+    keep = [i for i in range(M) if i not in (4, 9, 20)]
+    assert torch.isnan(t.scale[[4, 9, 20]]).all() and not t.codes[[4, 9, 20]].any()
+    assert torch.isnan(y[[4, 9, 20]]).all() and torch.equal(y[keep], y0[keep])
+    assert torch.isnan(q.int8_dequantize(t)[[4, 9, 20]]).all()
+
+
+# ---- forward
+FWD = [("bf16", 1, 64, 64, 8), ("f16", 1, 1, 64, 1), ("bf16", 2, 100, 128, 16), ("bf16", 16, 257, 320, 64),
+       ("f16", 13, 72, 4096, 128), ("bf16", 17, 64, 192, 24), ("bf16", 31, 100, 704, 100), ("f16", 33, 513, 64, 7),
+       ("bf16", 100, 129, 256, 64), ("bf16", 129, 300, 1152, 0), ("f16", 257, 264, 448, 40), ("bf16", 300, 777, 960, 128),
+       ("bf16", 1, 1000, 8256, 0), ("bf16", 520, 1032, 832, 16), ("f16", 8, 4096, 4096, 16), ("bf16", 5, 33, 11008, 12),
+       ("bf16", 64, 2048, 2048, 64), ("bf16", 3, 40, 28672, 64), ("f16", 16, 48, 16448, 5)]
+
+
+@pytest.mark.parametrize("fmt,M,N,K,r", FWD)
+def test_forward(q, fmt, M, N, K, r):
+    say(f"[int8 fwd] {fmt} M={M} N={N} K={K} r={r}")
+    L = Layer(q, fmt, 1000 + M + N, M, N, K, r)
+    keep = q.Int8Tensor.empty(M, K, dtype=L.x.dtype)
+    y, t = q.int8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha, keep=keep)
+    assert np.array_equal(keep.codes.cpu().numpy(), L.cx) and np.array_equal(keep.scale.cpu().numpy(), L.sx)
+    if r:
+        L.check_t(t)
+    L.check_y(y, t)
+    y2, t2 = q.int8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha, want_t=False)   # nothing kept
+    assert t2 is None
+    L.check_y(y2)
+    L.check_y(q.int8_gemm_fwd(L.w, keep, t, L.B), t)                        # the product for a given t
+
+
+# ---- backward
+DX = [("bf16", 1, 64, 64, 8), ("f16", 5, 1, 64, 3), ("bf16", 33, 100, 128, 16), ("bf16", 129, 257, 320, 64),
+      ("f16", 64, 1000, 192, 24), ("bf16", 257, 72, 704, 100), ("bf16", 300, 513, 960, 0), ("f16", 520, 264, 1152, 128),
+      ("bf16", 100, 3001, 64, 7), ("bf16", 17, 4096, 512, 64), ("bf16", 600, 640, 1344, 40)]
+
+
+@pytest.mark.parametrize("fmt,M,N,K,r", DX)
+def test_input_gradient(q, fmt, M, N, K, r):
+    say(f"[int8 dx] {fmt} M={M} N={N} K={K} r={r}")
+    L = Layer(q, fmt, 3000 + M + N, M, N, K, r)
+    u, dx = q.int8_linear_bwd_dx(L.w, L.A, L.B, L.alpha, L.dy)
+    if r:
+        L.check_u(u)
+    L.check_dx(dx, u)
+    L.check_dx(q.int8_gemm_bwd_dx(L.w, L.dy, u, L.A), u)
+
+
+GRADS = [("bf16", 8, [(1, 64, 64)]), ("f16", 3, [(70, 100, 128), (2, 1, 64)]), ("bf16", 64, [(500, 257, 320)] * 3),
+         ("bf16", 100, [(129, 72, 192), (1030, 520, 64)]), ("f16", 128, [(65, 64, 576)]),
+         ("bf16", 24, [(2050, 136, 256), (33, 1001, 128)]), ("bf16", 1, [(300, 64, 64)]), ("f16", 33, [(64, 40, 4160)])]
+
+
+@pytest.mark.parametrize("fmt,r,shapes", GRADS)
+def test_gradients_from_checkpoints(q, fmt, r, shapes):
+    say(f"[int8 grads] {fmt} r={r} {shapes}")
+    Ls = [Layer(q, fmt, 5000 + 10 * i + r, M, N, K, r) for i, (M, N, K) in enumerate(shapes)]
+    recs = []
+    for i, L in enumerate(Ls):
+        recs.append((q.int8_quantize(L.x), L.dev(bits(fmt, 70 + i, (L.M, r))), L.dev(bits(fmt, 90 + i, (L.M, r))), L.dy))
+    dA, dB = q.lora_grads_batch_int8(recs)
+    again = q.lora_grads_batch_int8(recs)
+    for i, L in enumerate(Ls):
+        L.check_grads(dA[i], dB[i], recs[i][1], recs[i][2])
+        assert (f64(dA[i]) == f64(again[0][i])).all() and (f64(dB[i]) == f64(again[1][i])).all()
+
+
+def test_many_layers_and_an_empty_one(q):
+    """Eighteen layers with an empty one among them (zero gradients, no pointers needed for its inputs)."""
+    import torch
+    say("[int8 grads] eighteen layers")
+    r = 16
+    Ls = [Layer(q, "bf16", 6000 + 10 * i, 40 + 9 * i, 64 + 8 * i, 64 * (1 + i % 3), r) for i in range(17)]
+    recs = [(q.int8_quantize(L.x), L.dev(bits("bf16", 7 + i, (L.M, r))), L.dev(bits("bf16", 50 + i, (L.M, r))), L.dy)
+            for i, L in enumerate(Ls)]
+    e = lambda n: torch.empty((0, n), dtype=torch.bfloat16, device="cuda:0")
+    recs.insert(5, (q.int8_quantize(e(192)), e(r), e(r), e(72)))
+    dA, dB = q.lora_grads_batch_int8(recs)
+    assert dA[5].shape == (192, r) and not dA[5].any() and not dB[5].any()
+    for i, L in enumerate(Ls):
+        j = i + (i >= 5)
+        L.check_grads(dA[j], dB[j], recs[j][1], recs[j][2])
+
+
+def test_no_tokens(q):
+    import torch
+    say("[int8] no tokens")
+    L = Layer(q, "bf16", 40, 4, 72, 128, 8)
+    e = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda:0")
+    y, t = q.int8_linear_fwd(L.w, e, L.A, L.B, 1.0, keep=q.Int8Tensor.empty(0, 128))
+    u, dx = q.int8_linear_bwd_dx(L.w, L.A, L.B, 1.0, torch.empty((0, 72), dtype=torch.bfloat16, device="cuda:0"))
+    assert y.shape == (0, 72) and t.shape == (0, 8) and u.shape == (0, 8) and dx.shape == (0, 128)
+    assert q.int8_dequantize(q.int8_quantize(e)).shape == (0, 128)
+
+
+# ---- as they are used together
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+def test_training_step_of_a_block(q, fmt):
+    """Forward with checkpoints, x freed, input gradients per layer, every dA and dB at the end; an NF4 layer's
+    gradients come from a checkpoint too."""
+    say(f"[int8 step] {fmt}")
+    r, alpha = 24, 48.0
+    shapes = [(200, 320, 512), (200, 192, 512), (130, 512, 256)]
+    Ls = [Layer(q, fmt, 8000 + 10 * i, M, N, K, r, alpha) for i, (M, N, K) in enumerate(shapes)]
+    kept = []
+    for L in Ls:
+        ck = q.Int8Tensor.empty(L.M, L.K, dtype=L.x.dtype)
+        y, t = q.int8_linear_fwd(L.w, L.x, L.A, L.B, alpha, keep=ck)
+        L.check_y(y, t)
+        L.x.fill_(float("nan"))                                    # the backward has no use for x
+        kept.append((ck, t))
+    recs = []
+    for L, (ck, t) in zip(Ls, kept):
+        u, dx = q.int8_linear_bwd_dx(L.w, L.A, L.B, alpha, L.dy)
+        L.check_dx(dx, u)
+        recs.append((ck, t, u, L.dy))
+    L = Ls[0]
+    w4 = q.quantize(L.dev(L.wb))
+    u4, _ = q.linear_bwd_dx(w4, L.A, L.B, alpha, L.dy)
+    recs.append((kept[0][0], kept[0][1], u4, L.dy))
+    dA, dB = q.lora_grads_batch_int8(recs)
+    for i, L in enumerate(Ls + [Ls[0]]):
+        L.check_grads(dA[i], dB[i], recs[i][1], recs[i][2])
+    # the gradients of lora_grads_batch on the restored x are those of the checkpoint, up to the order of fp32 sums
+    L, ck = Ls[0], kept[0][0]
+    dA16, dB16 = q.lora_grads_batch([(q.int8_dequantize(ck), recs[0][1], recs[0][2], L.dy)])
+    L.check_grads(dA16[0], dB16[0], recs[0][1], recs[0][2])
+
+
+@pytest.mark.parametrize("M", [200, 9])
+def test_captured_step_replays_match_eager(q, M):
+    """Forward, input gradient and gradients in one graph on one workspace; eager calls of the same layer between
+    the replays; two graphs that share the workspace, replayed in turn."""
+    import torch
+    say(f"[int8 graph] M={M}")
+    N, K, r, alpha = 320, 512, 16, 32.0
+    L = Layer(q, "bf16", 8500 + M, M, N, K, r, alpha)
+    bf = torch.bfloat16
+    out = dict(y=torch.empty((M, N), dtype=bf, device="cuda:0"), t=torch.empty((M, r), dtype=bf, device="cuda:0"),
+               u=torch.empty((M, r), dtype=bf, device="cuda:0"), dx=torch.empty((M, K), dtype=bf, device="cuda:0"),
+               dA=torch.empty((K, r), device="cuda:0"), dB=torch.empty((r, N), device="cuda:0"))
+    ck = q.Int8Tensor.empty(M, K)
+    ws = torch.empty(1 << 23, dtype=torch.uint8, device="cuda:0")
+
+    def step():
+        q.int8_linear_fwd(L.w, L.x, L.A, L.B, alpha, y=out["y"], t=out["t"], keep=ck, ws=ws)
+        q.int8_linear_bwd_dx(L.w, L.A, L.B, alpha, L.dy, u=out["u"], dx=out["dx"], ws=ws)
+        q.lora_grads_batch_int8([(ck, out["t"], out["u"], L.dy)], dA=[out["dA"]], dB=[out["dB"]], ws=ws)
+
+    def snap():
+        torch.cuda.synchronize()
+        return {k: v.clone() for k, v in out.items()}
+
+    step()
+    eager = snap()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    for rep in range(4):
+        for v in out.values():
+            v.fill_(float("nan"))
+        ck.codes.zero_()
+        ws.fill_(0xA5)
+        torch.cuda.synchronize()
+        graphs[rep % 2].replay()
+        got = snap()
+        for k in out:
+            assert torch.equal(got[k], eager[k]), f"replay {rep}: {k} differs"
+        q.int8_linear_fwd(L.w, L.x, L.A, L.B, alpha, ws=ws)        # eager work on the same workspace
+
+
+def test_two_streams_at_once(q):
+    """Two layers on two streams, each with its own workspace: both are what they are alone."""
+    import torch
+    say("[int8] two streams")
+    Ls = [Layer(q, "bf16", 8700 + i, 150, 264, 640, 16) for i in range(2)]
+    alone = [q.int8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha) for L in Ls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Ls]
+    got = [[], []]
+    for _ in range(4):
+        for i, L in enumerate(Ls):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(q.int8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y, t in got[i]:
+            assert torch.equal(y, alone[i][0]) and torch.equal(t, alone[i][1])
+
+
+def test_offsets_past_32_bits(q):
+    """Activations and a weight of over 2^31 elements: the first and last rows against float64 on the device."""
+    import torch
+    say("[int8] offsets past 32 bits")
+    K, N = 65536, 33024
+    g = torch.Generator(device="cuda:0")
+    g.manual_seed(4)
+    x = torch.empty((N, K), dtype=torch.bfloat16, device="cuda:0")
+    for i in range(0, N, 4128):
+        x[i:i + 4128] = torch.randn((4128, K), generator=g, device="cuda:0").to(torch.bfloat16)
+    big = q.int8_quantize(x)
+    rows = [0, 1, 32767, 32768, N - 2, N - 1]
+    part = x[rows].contiguous()
+    small = q.int8_quantize(part)
+    assert torch.equal(big.codes[rows], small.codes) and torch.equal(big.scale[rows], small.scale)
+    back = q.int8_dequantize(big)
+    assert torch.equal(back[rows], q.int8_dequantize(small))
+    h = 2.0 ** -8
+    for M in (1, 40):
+        xs = x[N - M:].contiguous()
+        xi = q.int8_quantize(xs)
+        y = q.int8_gemm_fwd(big, xi)                                 # N x K weight
+        want = torch.mm(xi.codes.double() * xi.scale.double()[:, None],
+                        (small.codes.double() * small.scale.double()[:, None]).t().contiguous())
+        assert bool(((y[:, rows].double() - want).abs() <= want.abs() * (h + 2.0 ** -20)).all())
+        dy = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda:0")
+        dy[:, rows] = torch.randn((M, 6), generator=g, device="cuda:0").to(torch.bfloat16)
+        dx = q.int8_gemm_bwd_dx(big, dy)
+        d, w = dy[:, rows].double(), back[rows].double()
+        tol = (h * torch.mm(d, w).abs() + (N + 8) * 2.0 ** -23 * torch.mm(d.abs(), w.abs())) * (1 + 2 * h)
+        assert bool(((dx.double() - torch.mm(d, w)).abs() <= tol).all())
+    wsm = q.int8_quantize(part[:2])                                  # M of over 2^31 elements
+    y = q.int8_gemm_fwd(wsm, big)
+    want = torch.mm(small.codes.double() * small.scale.double()[:, None],
+                    (wsm.codes.double() * wsm.scale.double()[:, None]).t().contiguous())
+    assert bool(((y[rows].double() - want).abs() <= want.abs() * (h + 2.0 ** -20)).all())
