@@ -44,40 +44,6 @@ __device__ __forceinline__ u32x4_t col8(const uint16_t* __restrict__ p, int64_t 
     return u32x4_t{w[0], w[1], w[2], w[3]};
 }
 
-// One wave per 32 x 32 outputs, operands straight from memory: lane (h, l32) holds row
-// l32 and 16 bytes k = 16 h .. of each 32-wide step.
-template <int DT>
-__global__ __launch_bounds__(64) void int8_fwd_simple_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx,
-                                                             const int8_t* __restrict__ wq,
-                                                             const float* __restrict__ sw,
-                                                             const uint16_t* __restrict__ t,
-                                                             const uint16_t* __restrict__ B, uint16_t* __restrict__ y,
-                                                             int M, int N, int K, int r, int tn) {
-    const int lane = threadIdx.x, h = lane >> 5, l32 = lane & 31;
-    const int m0 = (int)(blockIdx.x / tn) * 32, n0 = (int)(blockIdx.x % tn) * 32;
-    const int am = min(m0 + l32, M - 1), bn = min(n0 + l32, N - 1);
-    const int8_t* ap = xq + (int64_t)am * K + 16 * h;
-    const int8_t* bp = wq + (int64_t)bn * K + 16 * h;
-    i32x16_t acc;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0;
-    for (int k = 0; k < K; k += 32)
-        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(*reinterpret_cast<const i32x4_t*>(ap + k),
-                                                    *reinterpret_cast<const i32x4_t*>(bp + k), acc, 0, 0, 0);
-    const int n = n0 + l32;
-    const float s = sw[bn];
-    f32x16_t f;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) f[v] = (float)acc[v] * (sx[min(m0 + 8 * (v >> 2) + 4 * h + (v & 3), M - 1)] * s);
-    for (int j = 0; j < r; j += 16)
-        f = mfma32<DT>(row8(t, r, m0 + l32, m0 + l32 < M, j + 8 * h, r), col8(B, N, n, n < N, j + 8 * h, r), f);
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int m = m0 + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (m < M && n < N) y[(int64_t)m * N + n] = (uint16_t)(pack2<DT>(f[v], 0.0f) & 0xFFFFu);
-    }
-}
-
 template <int DT>
 __global__ __launch_bounds__(64) void int8_dx_simple_kernel(const uint16_t* __restrict__ dy,
                                                             const int8_t* __restrict__ wq,
@@ -114,19 +80,6 @@ __global__ __launch_bounds__(64) void int8_dx_simple_kernel(const uint16_t* __re
 }
 
 }  // namespace
-
-qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                                  const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
-                                  hipStream_t s) {
-    const int64_t tm = ((int64_t)M + 31) / 32, tn = ((int64_t)N + 31) / 32;
-    if (tm * tn >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED_SHAPE;
-    with_dt(dt, [&](auto dtc) {
-        constexpr int DT = decltype(dtc)::value;
-        hipLaunchKernelGGL(int8_fwd_simple_kernel<DT>, dim3((unsigned)(tm * tn)), dim3(64), 0, s, xq, sx, wq, sw, t, B,
-                           y, M, N, K, r, (int)tn);
-    });
-    return launch_status();
-}
 
 qlora_status launch_int8_gemm_bwd_dx(const uint16_t* dy, const int8_t* wq, const float* sw, const uint16_t* u,
                                      const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt,

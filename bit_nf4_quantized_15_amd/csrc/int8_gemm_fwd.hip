@@ -1,0 +1,329 @@
+// Forward product of the int8 layer on MFMA (v_mfma_i32_32x32x32_i8), gfx950:
+//
+//   y[m,n] = RNE_16( sx[m] sw[n] sum_k xq[m,k] wq[n,k] + sum_j t[m,j] B[j,n] )
+//
+// ("bitsandbytes deep dive", section 4: vector-wise int8; sections 8.6 / 12.4: the LoRA
+// branch.)  Both operands are int8 rows with consecutive k, so both tiles are copied
+// HBM -> LDS by direct loads (64 k per step, 16 bytes per lane, XOR-swizzled on the global
+// side) into a ring of four steps, and a lane's MFMA operand is one 16-byte LDS read.
+// Step ks requests tile ks + 3 and reads its own first operands before the barrier that
+// ends step ks - 1; that barrier only waits for the loads of two steps before, so neither
+// the loads nor the LDS latency is exposed.  Sums are exact int32; the scales, t B (r more
+// reduction steps of the 16-bit MFMA on the same accumulators) and the rounding follow
+// once per tile.
+//
+// W rows are the MFMA's first operand, so a lane holds one token m and groups of four
+// consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.
+#include "int8.h"
+
+namespace qlora {
+
+__device__ void raw_buffer_load_lds(i32x4_t rsrc, __attribute__((address_space(3))) uint32_t* lds_ptr, int size,
+                                    int voffset, int soffset, int offset, int aux) __asm("llvm.amdgcn.raw.buffer.load.lds");
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x16_t mfma16(u32x4_t a, u32x4_t b, f32x16_t c) {
+    if (DT == kDtF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
+                                                      c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+
+__device__ __forceinline__ i32x4_t buffer_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return i32x4_t{(int32_t)(uint32_t)a, (int32_t)(uint32_t)(a >> 32), (int32_t)bytes, 0x00020000};
+}
+
+// The cast keeps the pointer's origin, so that the compiler can tell a direct load's
+// destination from the buffers a step reads (each ring slot is an object of its own).
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(3))) T* as_lds(const void* p) {
+    return (__attribute__((address_space(3))) T*)(p);
+}
+
+constexpr int kStep = 64;   // reduction per step: bytes of a tile row
+constexpr int kRing = 4;
+
+// Byte of 16-byte chunk c of tile row `row`: 64-byte rows, chunks XOR-swizzled so that any
+// 16 consecutive rows of one chunk cover all 64 banks.
+__device__ __forceinline__ uint32_t tile_byte(int row, int c) {
+    return (uint32_t)row * 64u + ((uint32_t)(c ^ ((row >> 2) & 3)) << 4);
+}
+
+// Tiles in groups of `gm` row tiles, down the rows first: 32 consecutive tiles (one XCD's
+// CUs at a time) then form a block of gm x 32 / gm that shares panels in the XCD's L2.
+struct TileMap {
+    int tm, tn, gm;
+};
+__device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int& nt) {
+    const int total = tp.tm * tp.tn, xcd = bid & 7, idx = bid >> 3, per = total >> 3, rem = total & 7;
+    const int id = xcd * per + min(xcd, rem) + idx;   // workgroups are dealt round robin to the 8 XCDs
+    const int span = tp.gm * tp.tn, g = id / span, in = id - g * span, rows = min(tp.gm, tp.tm - g * tp.gm);
+    nt = in / rows;
+    mt = g * tp.gm + in - nt * rows;
+}
+
+// NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs.
+template <int NWM, int NWN, int MT, int NT, int DT>
+__global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gemm_fwd_kernel(
+    const int8_t* __restrict__ xq, const float* __restrict__ sx, const int8_t* __restrict__ wq,
+    const float* __restrict__ sw, const uint16_t* __restrict__ t, const uint16_t* __restrict__ B,
+    uint16_t* __restrict__ y, int M, int N, int K, int r, TileMap tp) {
+    constexpr int kWaves = NWM * NWN, kThreads = 64 * kWaves;
+    constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN;
+    constexpr int kXB = kBM * kStep, kWB = kBN * kStep;      // bytes of a step's tiles
+    constexpr int kXL = kXB / 1024 / kWaves, kWL = kWB / 1024 / kWaves;   // loads per wave
+    static_assert(kXL * kWaves * 1024 == kXB && kWL * kWaves * 1024 == kWB, "tiles are whole wave loads");
+    __shared__ __attribute__((aligned(16))) uint8_t s0[kXB + kWB];
+    __shared__ __attribute__((aligned(16))) uint8_t s1[kXB + kWB];
+    __shared__ __attribute__((aligned(16))) uint8_t s2[kXB + kWB];
+    __shared__ __attribute__((aligned(16))) uint8_t s3[kXB + kWB];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % NWM, wn = wave / NWM;
+    int mt, nt;
+    tile_of(tp, blockIdx.x, mt, nt);
+    const int m0 = mt * kBM, n0 = nt * kBN;
+    const int NS = K / kStep;
+
+    // panels as buffers: rows past the end read as zero (the range check covers voffset)
+    const i32x4_t xrs = buffer_rsrc(xq + (int64_t)m0 * K, (uint32_t)min(M - m0, kBM) * (uint32_t)K);
+    const i32x4_t wrs = buffer_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(N - n0, kBN) * (uint32_t)K);
+    // a wave load fills 16 rows of 64 bytes; lane: row lane / 4, LDS chunk lane % 4
+    const int lrow = lane >> 2, lch = (lane & 3) ^ ((lrow >> 2) & 3);
+    const uint32_t voff = (uint32_t)(16 * wave + lrow) * (uint32_t)K + 16u * (uint32_t)lch;
+    auto load = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < kXL; ++j)
+            raw_buffer_load_lds(xrs, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
+                                (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kWL; ++j)
+            raw_buffer_load_lds(wrs, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
+                                (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+    };
+    // operand bytes: chunk 2 kk + h of rows 32 i + l32 (the swizzle has period 16 rows)
+    uint32_t offX[2], offW[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        offX[kk] = tile_byte(32 * MT * wm + l32, 2 * kk + h);
+        offW[kk] = kXB + tile_byte(32 * NT * wn + l32, 2 * kk + h);
+    }
+    auto read = [&](const uint8_t* __restrict__ slot, int kk, i32x4_t (&a)[MT], i32x4_t (&b)[NT])
+                    __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) b[i] = *reinterpret_cast<const i32x4_t*>(slot + offW[kk] + 2048u * i);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const i32x4_t*>(slot + offX[kk] + 2048u * i);
+    };
+
+    i32x16_t acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+    load(s0, 0);
+    load(s1, min(1, NS - 1));
+    load(s2, min(2, NS - 1));
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");   // tiles 0 and 1 have landed
+    i32x4_t xa[2][MT], wb[2][NT];
+    read(s0, 0, xa[0], wb[0]);
+
+    auto step = [&](int ks, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
+                    uint8_t* __restrict__ fill) __attribute__((always_inline)) {
+        load(fill, min(ks + 3, NS - 1));
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if (kk == 0) read(cur, 1, xa[1], wb[1]);
+            else read(next, 0, xa[0], wb[0]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wb[kk][j], xa[kk][i], acc[i][j], 0, 0, 0);
+        }
+        // tile ks + 2 has landed once only this step's own loads are in flight
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
+    };
+    int ks = 0;
+    for (; ks + kRing <= NS; ks += kRing) {   // whole turns of the ring: no branch between its steps
+        step(ks, s0, s1, s3);
+        step(ks + 1, s1, s2, s0);
+        step(ks + 2, s2, s3, s1);
+        step(ks + 3, s3, s0, s2);
+    }
+    if (ks < NS) step(ks, s0, s1, s3);
+    if (ks + 1 < NS) step(ks + 1, s1, s2, s0);
+    if (ks + 2 < NS) step(ks + 2, s2, s3, s1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last, unused tiles
+    __syncthreads();
+
+    // ---- scales: sw[n] per register, sx[m] per lane
+    float* const swt = reinterpret_cast<float*>(s3);
+    for (int i = tid; i < kBN; i += kThreads) swt[i] = sw[min(n0 + i, N - 1)];
+    float sxv[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sxv[i] = sx[min(m0 + 32 * (MT * wm + i) + l32, M - 1)];
+    __syncthreads();
+    f32x16_t f[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+                const f32x4_t w4 =
+                    *reinterpret_cast<const f32x4_t*>(swt + 32 * (NT * wn + j) + 8 * v4 + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[i][j][4 * v4 + e] = (float)acc[i][j][4 * v4 + e] * (sxv[i] * w4[e]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one tile at a time: the accumulators fill the registers
+        }
+
+    // ---- LoRA: 32 more reduction indices j at a time; t rows in s0 (64-byte rows, the
+    // tiles' layout), B rows in their own layout in s1 and s2, read down their columns
+    constexpr int kBLd = 2 * kBN + 32;       // bytes of a staged row of B: rows start 8 banks apart
+    static_assert(16 * kBLd <= kXB + kWB && kBM * 64 <= kXB + kWB, "LoRA operands fit the ring slots");
+    const bool tvec = (r & 7) == 0, nvec = (N & 7) == 0;
+    const int tj = l32 & 15, tg = l32 >> 4;
+    for (int j0 = 0; j0 < r; j0 += 32) {
+        for (int c = tid; c < kBM * 4; c += kThreads) {
+            const int row = c >> 2, j = j0 + 8 * (c & 3), m = m0 + row;
+            u32x4_t v = {0u, 0u, 0u, 0u};
+            if (m < M && j < r) {
+                const uint16_t* p = t + (int64_t)m * r + j;
+                if (tvec) {
+                    v = *reinterpret_cast<const u32x4_t*>(p);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (j + i < r) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+                }
+            }
+            *reinterpret_cast<u32x4_t*>(s0 + tile_byte(row, c & 3)) = v;
+        }
+        for (int c = tid; c < 32 * (kBN / 8); c += kThreads) {
+            const int row = c / (kBN / 8), j = j0 + row, cc = c % (kBN / 8), n = n0 + 8 * cc;
+            u32x4_t v = {0u, 0u, 0u, 0u};
+            if (j < r && n < N) {
+                const uint16_t* p = B + (int64_t)j * N + n;
+                if (nvec) {
+                    v = *reinterpret_cast<const u32x4_t*>(p);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i < N) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+                }
+            }
+            *reinterpret_cast<u32x4_t*>((row < 16 ? s1 : s2) + (row & 15) * kBLd + 16 * cc) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            // rows j0 + 16 kk + 8 h .. + 7 of B, column l32 of each tile: two transposed reads
+            u32x4_t b[NT], a[MT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint8_t* p = (kk ? s2 : s1) + (8 * h + (tj >> 2)) * kBLd +
+                                   2 * (32 * (NT * wn + j) + 16 * tg + 4 * (tj & 3));
+                const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p));
+                const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p + 4 * kBLd));
+                b[j] = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const u32x4_t*>(s0 + offX[kk] + 2048u * i);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) f[i][j] = mfma16<DT>(b[j], a[i], f[i][j]);
+        }
+        __syncthreads();
+    }
+
+    // ---- y: lane (h, l32) holds token 32 i + l32, outputs 32 j + 8 v4 + 4 h + 0..3
+    if (!nvec) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m0 + 32 * (MT * wm + i) + l32;
+            if (m >= M) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int n = n0 + 32 * (NT * wn + j) + 8 * (v >> 2) + 4 * h + (v & 3);
+                    if (n < N) y[(int64_t)m * N + n] = (uint16_t)(pack2<DT>(f[i][j][v], 0.0f) & 0xFFFFu);
+                }
+        }
+        return;
+    }
+    // Through LDS, one 32-token tile of every wave row at a time (each in a slot of its own:
+    // NWM * 32 rows of kBN outputs, rows padded by 16 bytes), then 16-byte stores of whole rows.
+    constexpr int kYLd = 2 * kBN + 16;
+    static_assert(32 * kYLd <= kXB + kWB && NWM <= 2, "a wave row's tokens fit a slot");
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        uint8_t* const slot = wm == 0 ? ((i & 1) ? s2 : s0) : ((i & 1) ? s3 : s1);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+                const u32x2_t o = {pack2<DT>(f[i][j][4 * v4], f[i][j][4 * v4 + 1]),
+                                   pack2<DT>(f[i][j][4 * v4 + 2], f[i][j][4 * v4 + 3])};
+                *reinterpret_cast<u32x2_t*>(slot + l32 * kYLd + 2 * (32 * (NT * wn + j) + 8 * v4 + 4 * h)) = o;
+            }
+        __syncthreads();   // the slot written two tiles ago was read before the last barrier
+#pragma unroll
+        for (int e = 0; e < (NWM * 32 * (kBN / 8) + kThreads - 1) / kThreads; ++e) {
+            const int c = tid + kThreads * e;
+            if (NWM * 32 * (kBN / 8) % kThreads && c >= NWM * 32 * (kBN / 8)) break;
+            const int cc = c % (kBN / 8), rr = c / (kBN / 8), w = rr >> 5, row = rr & 31;
+            const int m = m0 + 32 * (MT * w + i) + row, n = n0 + 8 * cc;
+            const uint8_t* src = (w == 0 ? ((i & 1) ? s2 : s0) : ((i & 1) ? s3 : s1)) + row * kYLd + 16 * cc;
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+            if (m < M && n < N) *reinterpret_cast<u32x4_t*>(y + (int64_t)m * N + n) = v;
+        }
+    }
+}
+
+template <int NWM, int NWN, int MT, int NT>
+qlora_status run(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const uint16_t* t,
+                 const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt, hipStream_t s) {
+    constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN;
+    TileMap tp;
+    tp.tm = (int)(((int64_t)M + kBM - 1) / kBM);
+    tp.tn = (int)(((int64_t)N + kBN - 1) / kBN);
+    tp.gm = 4;
+    const int64_t total = (int64_t)tp.tm * tp.tn;
+    if (total * 64 * NWM * NWN >= (int64_t(1) << 32) || (int64_t)tp.gm * tp.tn >= (int64_t(1) << 31))
+        return QLORA_ERR_UNSUPPORTED_SHAPE;
+    with_dt(dt, [&](auto dtc) {
+        constexpr int DT = decltype(dtc)::value;
+        hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, DT>), dim3((unsigned)total),
+                           dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
+    });
+    return launch_status();
+}
+
+}  // namespace
+
+qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                  const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
+                                  hipStream_t s) {
+    const int64_t big = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
+    const int64_t mid = (((int64_t)M + 127) / 128) * (((int64_t)N + 127) / 128);
+    if (big >= 200) return run<2, 2, 4, 4>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
+    if (mid >= 200 && M > 64) return run<2, 2, 2, 2>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
+    return run<2, 2, 1, 1>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
+}
+
+}  // namespace qlora
