@@ -13,7 +13,9 @@
 // once per tile.
 //
 // W rows are the MFMA's first operand, so a lane holds one token m and groups of four
-// consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.
+// consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.  t, the
+// first 64 rows of B and the scales are fetched before the main loop into registers that it
+// has no use for, and the epilogue goes 32 tokens at a time (scale, t B, round, store).
 #include "int8.h"
 
 namespace qlora {
@@ -35,6 +37,20 @@ __device__ __forceinline__ f32x16_t mfma16(u32x4_t a, u32x4_t b, f32x16_t c) {
                                                    0, 0);
 }
 
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t buf_rsrc(const void* p, uint64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes, 0x00020000);
+}
+
+// 8 values p[i .. i + 7] of a row whose values end at `end`, zero past it.
+__device__ __forceinline__ u32x4_t load8(const uint16_t* __restrict__ p, int i, int end) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (i + e < end) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    return v;
+}
 
 __device__ __forceinline__ i32x4_t buffer_rsrc(const void* base, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -70,8 +86,9 @@ __device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int
     mt = g * tp.gm + in - nt * rows;
 }
 
-// NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs.
-template <int NWM, int NWN, int MT, int NT, int DT>
+// NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs.  VEC: r % 8 == 0 and
+// N % 8 == 0, so t, B and y are accessed 16 bytes at a time.
+template <int NWM, int NWN, int MT, int NT, bool VEC, int DT>
 __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gemm_fwd_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ sx, const int8_t* __restrict__ wq,
     const float* __restrict__ sw, const uint16_t* __restrict__ t, const uint16_t* __restrict__ B,
@@ -85,6 +102,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
     __shared__ __attribute__((aligned(16))) uint8_t s1[kXB + kWB];
     __shared__ __attribute__((aligned(16))) uint8_t s2[kXB + kWB];
     __shared__ __attribute__((aligned(16))) uint8_t s3[kXB + kWB];
+    __shared__ __attribute__((aligned(16))) float swt[kBN];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % NWM, wn = wave / NWM;
@@ -100,13 +118,16 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
     const int lrow = lane >> 2, lch = (lane & 3) ^ ((lrow >> 2) & 3);
     const uint32_t voff = (uint32_t)(16 * wave + lrow) * (uint32_t)K + 16u * (uint32_t)lch;
     auto load = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
+        i32x4_t xr = xrs, wr = wrs;
+        xr[2] = ks < NS ? xr[2] : 0;   // steps past K read as zero and move nothing
+        wr[2] = ks < NS ? wr[2] : 0;
 #pragma unroll
         for (int j = 0; j < kXL; ++j)
-            raw_buffer_load_lds(xrs, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
+            raw_buffer_load_lds(xr, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
                                 (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
 #pragma unroll
         for (int j = 0; j < kWL; ++j)
-            raw_buffer_load_lds(wrs, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
+            raw_buffer_load_lds(wr, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
                                 (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
     };
     // operand bytes: chunk 2 kk + h of rows 32 i + l32 (the swizzle has period 16 rows)
@@ -124,6 +145,40 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
         for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const i32x4_t*>(slot + offX[kk] + 2048u * i);
     };
 
+    // ---- ahead of the main loop: scales, t as MFMA operands (lane: token l32, ranks 8 h .. of
+    // each 16) and the first 64 rows of B, 16 bytes along n per lane
+    for (int i = tid; i < kBN; i += kThreads) swt[i] = sw[min(n0 + i, N - 1)];
+    float sxv[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sxv[i] = sx[min(m0 + 32 * (MT * wm + i) + l32, M - 1)];
+    const rsrc_t trs = buf_rsrc(r ? t + (int64_t)m0 * r : nullptr, (uint64_t)min(M - m0, kBM) * r * 2);
+    auto load_t = [&](int i, int kk) __attribute__((always_inline)) {
+        const int row = 32 * (MT * wm + i) + l32, j = 16 * kk + 8 * h;
+        if (VEC)
+            return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   trs, j < r ? (uint32_t)(row * r + j) * 2u : 0x80000000u, 0, 0));
+        return m0 + row < M && j < r ? load8(t + (int64_t)(m0 + row) * r + j, j, r) : u32x4_t{0u, 0u, 0u, 0u};
+    };
+    const rsrc_t brs = buf_rsrc(r ? B + n0 : nullptr, r ? ((uint64_t)r * N - n0) * 2 : 0);
+    constexpr int kCh = kBN / 8, kBPer = 64 * kCh / kThreads;   // 16-byte chunks of a row; per thread of 64 rows
+    auto load_b = [&](int j0, int e) __attribute__((always_inline)) {
+        const int c = tid + kThreads * e, j = j0 + c / kCh, n = 8 * (c % kCh);
+        if (VEC)
+            return __builtin_bit_cast(u32x4_t,
+                                      __builtin_amdgcn_raw_buffer_load_b128(
+                                          brs, j < r && n0 + n < N ? ((uint32_t)j * N + n) * 2u : 0x80000000u, 0, 0));
+        return j < r && n0 + n < N ? load8(B + (int64_t)j * N + n0 + n, n0 + n, N) : u32x4_t{0u, 0u, 0u, 0u};
+    };
+    u32x4_t tv[MT][4], bv[kBPer];
+    if (r) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tv[i][kk] = load_t(i, kk);
+#pragma unroll
+        for (int e = 0; e < kBPer; ++e) bv[e] = load_b(0, e);
+    }
+
     i32x16_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -133,15 +188,16 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 
     load(s0, 0);
-    load(s1, min(1, NS - 1));
-    load(s2, min(2, NS - 1));
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");   // tiles 0 and 1 have landed
+    load(s1, 1);
+    load(s2, 2);
+    // tiles 0 and 1 have landed (and the scales are in swt)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
     i32x4_t xa[2][MT], wb[2][NT];
     read(s0, 0, xa[0], wb[0]);
 
     auto step = [&](int ks, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
                     uint8_t* __restrict__ fill) __attribute__((always_inline)) {
-        load(fill, min(ks + 3, NS - 1));
+        load(fill, ks + 3);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             if (kk == 0) read(cur, 1, xa[1], wb[1]);
@@ -151,145 +207,111 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wb[kk][j], xa[kk][i], acc[i][j], 0, 0, 0);
+            // the next half's operands are read (and the new tiles requested) between the MFMAs
+            constexpr int kReads = MT + NT, kPer = MT * NT / kReads;
+#pragma unroll
+            for (int g = 0; g < kReads; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                if (kk == 0) __builtin_amdgcn_sched_group_barrier(0x010, (kXL + kWL + kReads - 1) / kReads, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer > 0 ? kPer : 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // tile ks + 2 has landed once only this step's own loads are in flight
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    int ks = 0;
-    for (; ks + kRing <= NS; ks += kRing) {   // whole turns of the ring: no branch between its steps
+    // whole turns of the ring: steps past K multiply zeros
+    for (int ks = 0; ks < NS; ks += kRing) {
         step(ks, s0, s1, s3);
         step(ks + 1, s1, s2, s0);
         step(ks + 2, s2, s3, s1);
         step(ks + 3, s3, s0, s2);
     }
-    if (ks < NS) step(ks, s0, s1, s3);
-    if (ks + 1 < NS) step(ks + 1, s1, s2, s0);
-    if (ks + 2 < NS) step(ks + 2, s2, s3, s1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last, unused tiles
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last, empty tiles
     __syncthreads();
 
-    // ---- scales: sw[n] per register, sx[m] per lane
-    float* const swt = reinterpret_cast<float*>(s3);
-    for (int i = tid; i < kBN; i += kThreads) swt[i] = sw[min(n0 + i, N - 1)];
-    float sxv[MT];
+    // ---- epilogue.  B rows go to s1 (0 - 63) and s2 (64 - 127) in their own layout, 16-byte
+    // chunks swizzled by row; y leaves through s0 and s3 in turn, 32 tokens of each wave row.
+    constexpr int kBRow = 2 * kBN;
+    static_assert(64 * kBRow <= kXB + kWB && NWM * 32 * kBRow <= kXB + kWB, "epilogue tiles fit the ring slots");
+    auto put_b = [&](uint8_t* slot, int e, u32x4_t v) __attribute__((always_inline)) {
+        const int c = tid + kThreads * e, row = c / kCh, cc = c % kCh;
+        *reinterpret_cast<u32x4_t*>(slot + row * kBRow + 16 * (cc ^ ((row & 3) << 1))) = v;
+    };
+    if (r) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sxv[i] = sx[min(m0 + 32 * (MT * wm + i) + l32, M - 1)];
-    __syncthreads();
-    f32x16_t f[MT][NT];
+        for (int e = 0; e < kBPer; ++e) put_b(s1, e, bv[e]);
+        if (r > 64) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+            for (int e = 0; e < kBPer; ++e) bv[e] = load_b(64, e);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-                const f32x4_t w4 =
-                    *reinterpret_cast<const f32x4_t*>(swt + 32 * (NT * wn + j) + 8 * v4 + 4 * h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[i][j][4 * v4 + e] = (float)acc[i][j][4 * v4 + e] * (sxv[i] * w4[e]);
-            }
-            __builtin_amdgcn_sched_barrier(0);   // one tile at a time: the accumulators fill the registers
-        }
-
-    // ---- LoRA: 32 more reduction indices j at a time; t rows in s0 (64-byte rows, the
-    // tiles' layout), B rows in their own layout in s1 and s2, read down their columns
-    constexpr int kBLd = 2 * kBN + 32;       // bytes of a staged row of B: rows start 8 banks apart
-    static_assert(16 * kBLd <= kXB + kWB && kBM * 64 <= kXB + kWB, "LoRA operands fit the ring slots");
-    const bool tvec = (r & 7) == 0, nvec = (N & 7) == 0;
-    const int tj = l32 & 15, tg = l32 >> 4;
-    for (int j0 = 0; j0 < r; j0 += 32) {
-        for (int c = tid; c < kBM * 4; c += kThreads) {
-            const int row = c >> 2, j = j0 + 8 * (c & 3), m = m0 + row;
-            u32x4_t v = {0u, 0u, 0u, 0u};
-            if (m < M && j < r) {
-                const uint16_t* p = t + (int64_t)m * r + j;
-                if (tvec) {
-                    v = *reinterpret_cast<const u32x4_t*>(p);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (j + i < r) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-                }
-            }
-            *reinterpret_cast<u32x4_t*>(s0 + tile_byte(row, c & 3)) = v;
-        }
-        for (int c = tid; c < 32 * (kBN / 8); c += kThreads) {
-            const int row = c / (kBN / 8), j = j0 + row, cc = c % (kBN / 8), n = n0 + 8 * cc;
-            u32x4_t v = {0u, 0u, 0u, 0u};
-            if (j < r && n < N) {
-                const uint16_t* p = B + (int64_t)j * N + n;
-                if (nvec) {
-                    v = *reinterpret_cast<const u32x4_t*>(p);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (n + i < N) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-                }
-            }
-            *reinterpret_cast<u32x4_t*>((row < 16 ? s1 : s2) + (row & 15) * kBLd + 16 * cc) = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            // rows j0 + 16 kk + 8 h .. + 7 of B, column l32 of each tile: two transposed reads
-            u32x4_t b[NT], a[MT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint8_t* p = (kk ? s2 : s1) + (8 * h + (tj >> 2)) * kBLd +
-                                   2 * (32 * (NT * wn + j) + 16 * tg + 4 * (tj & 3));
-                const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p));
-                const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p + 4 * kBLd));
-                b[j] = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const u32x4_t*>(s0 + offX[kk] + 2048u * i);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) f[i][j] = mfma16<DT>(b[j], a[i], f[i][j]);
+            for (int e = 0; e < kBPer; ++e) put_b(s2, e, bv[e]);
         }
         __syncthreads();
     }
-
-    // ---- y: lane (h, l32) holds token 32 i + l32, outputs 32 j + 8 v4 + 4 h + 0..3
-    if (!nvec) {
+    const int tj = l32 & 15, tg = l32 >> 4;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < MT; ++i) {
+        f32x16_t f[NT];
+        // 256 sums live in the accumulation registers until their turn (the compiler would
+        // move all of them to vector registers at the end of the loop, and spill)
+        if constexpr (MT * NT >= 16)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+                const f32x4_t w4 = *reinterpret_cast<const f32x4_t*>(swt + 32 * (NT * wn + j) + 8 * v4 + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[j][4 * v4 + e] = (float)acc[i][j][4 * v4 + e] * (sxv[i] * w4[e]);
+            }
+        // t B: rows 16 kk + 8 h .. + 7 of B, column l32 of each tile, by two transposed reads
+        auto rank16 = [&](const uint8_t* slot, int kk, u32x4_t a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int row = 16 * kk + 8 * h + (tj >> 2), col = 32 * (NT * wn + j) + 16 * tg + 4 * (tj & 3);
+                const uint8_t* p = slot + row * kBRow + 16 * ((col >> 3) ^ ((row & 3) << 1)) + 2 * (col & 7);
+                const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p));
+                const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(as_lds<s16x4_t>(p + 4 * kBRow));
+                const u32x4_t b = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                f[j] = mfma16<DT>(b, a, f[j]);
+            }
+        };
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            if (16 * kk < r) rank16(s1, kk, tv[i][kk]);
+        for (int kk = 4; 16 * kk < r; ++kk) rank16(s2, kk - 4, load_t(i, kk));
+        // lane (h, l32): token l32 of the 32, outputs 32 j + 8 v4 + 4 h + 0..3
+        if (!VEC) {
             const int m = m0 + 32 * (MT * wm + i) + l32;
-            if (m >= M) continue;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int n = n0 + 32 * (NT * wn + j) + 8 * (v >> 2) + 4 * h + (v & 3);
-                    if (n < N) y[(int64_t)m * N + n] = (uint16_t)(pack2<DT>(f[i][j][v], 0.0f) & 0xFFFFu);
+                    if (m < M && n < N) y[(int64_t)m * N + n] = (uint16_t)(pack2<DT>(f[j][v], 0.0f) & 0xFFFFu);
                 }
+            continue;
         }
-        return;
-    }
-    // Through LDS, one 32-token tile of every wave row at a time (each in a slot of its own:
-    // NWM * 32 rows of kBN outputs, rows padded by 16 bytes), then 16-byte stores of whole rows.
-    constexpr int kYLd = 2 * kBN + 16;
-    static_assert(32 * kYLd <= kXB + kWB && NWM <= 2, "a wave row's tokens fit a slot");
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        uint8_t* const slot = wm == 0 ? ((i & 1) ? s2 : s0) : ((i & 1) ? s3 : s1);
+        uint8_t* const slot = (i & 1) ? s3 : s0;
+        constexpr int kMask = (kCh < 16 ? kCh : 16) - 1;   // 16-byte chunks of a row are swizzled by the token
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4) {
-                const u32x2_t o = {pack2<DT>(f[i][j][4 * v4], f[i][j][4 * v4 + 1]),
-                                   pack2<DT>(f[i][j][4 * v4 + 2], f[i][j][4 * v4 + 3])};
-                *reinterpret_cast<u32x2_t*>(slot + l32 * kYLd + 2 * (32 * (NT * wn + j) + 8 * v4 + 4 * h)) = o;
+                const u32x2_t o = {pack2<DT>(f[j][4 * v4], f[j][4 * v4 + 1]),
+                                   pack2<DT>(f[j][4 * v4 + 2], f[j][4 * v4 + 3])};
+                const int cc = 4 * (NT * wn + j) + v4;
+                *reinterpret_cast<u32x2_t*>(slot + (32 * wm + l32) * kBRow + 16 * (cc ^ (l32 & kMask)) + 8 * h) = o;
             }
-        __syncthreads();   // the slot written two tiles ago was read before the last barrier
+        __syncthreads();   // the slot written two rounds ago was read before the last barrier
 #pragma unroll
-        for (int e = 0; e < (NWM * 32 * (kBN / 8) + kThreads - 1) / kThreads; ++e) {
-            const int c = tid + kThreads * e;
-            if (NWM * 32 * (kBN / 8) % kThreads && c >= NWM * 32 * (kBN / 8)) break;
-            const int cc = c % (kBN / 8), rr = c / (kBN / 8), w = rr >> 5, row = rr & 31;
-            const int m = m0 + 32 * (MT * w + i) + row, n = n0 + 8 * cc;
-            const uint8_t* src = (w == 0 ? ((i & 1) ? s2 : s0) : ((i & 1) ? s3 : s1)) + row * kYLd + 16 * cc;
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+        for (int e = 0; e < NWM * 32 * kCh / kThreads; ++e) {
+            const int c = tid + kThreads * e, cc = c % kCh, rr = c / kCh;
+            const int m = m0 + 32 * (MT * (rr >> 5) + i) + (rr & 31), n = n0 + 8 * cc;
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(slot + rr * kBRow + 16 * (cc ^ (rr & kMask)));
             if (m < M && n < N) *reinterpret_cast<u32x4_t*>(y + (int64_t)m * N + n) = v;
         }
     }
@@ -306,10 +328,16 @@ qlora_status run(const int8_t* xq, const float* sx, const int8_t* wq, const floa
     const int64_t total = (int64_t)tp.tm * tp.tn;
     if (total * 64 * NWM * NWN >= (int64_t(1) << 32) || (int64_t)tp.gm * tp.tn >= (int64_t(1) << 31))
         return QLORA_ERR_UNSUPPORTED_SHAPE;
+    // (the offsets of B must fit a buffer's 31 bits)
+    const bool vec = r % 8 == 0 && N % 8 == 0 && (int64_t)r * N * 2 < (int64_t(1) << 31);
     with_dt(dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
-        hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, DT>), dim3((unsigned)total),
-                           dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
+        if (vec)
+            hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, true, DT>), dim3((unsigned)total),
+                               dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
+        else
+            hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, false, DT>), dim3((unsigned)total),
+                               dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
     });
     return launch_status();
 }
