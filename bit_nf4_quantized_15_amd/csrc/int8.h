@@ -38,4 +38,26 @@ qlora_status launch_int8_gemm_bwd_dx(const uint16_t* dy, const int8_t* wq, const
                                      const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt,
                                      hipStream_t s);
 
+// LoRA gradients from 8-bit checkpoints: up to kInt8GradLayers layers (two contractions each)
+// in one launch.  A contraction out[d, j] = sum_m X[m, d] S[m, j] takes codes with a scale per
+// row (out [D, r]) or, scale null, 16-bit values (out [r, D]).  all_tiles is the number of
+// 128-column tiles of the whole launch; the workspace of ws bytes needs no clearing.
+constexpr int kInt8GradLayers = 8;
+constexpr int kInt8GradChunk = 4096;   // rows per workgroup at most (their scales sit in LDS)
+struct Int8GradPlan {
+    int64_t tiles, splits, chunk;
+    size_t ws_tags, ws;
+};
+Int8GradPlan plan_int8_grad(int64_t M, int64_t D, int r, int64_t all_tiles);
+struct Int8GradDesc {
+    const void* X;
+    const float* scale;
+    const uint16_t* S;
+    float* out;
+    void* ws;
+    int M, D;
+    Int8GradPlan plan;
+};
+qlora_status launch_int8_grads(const Int8GradDesc* d, int count, int r, int dt, hipStream_t s);
+
 }  // namespace qlora

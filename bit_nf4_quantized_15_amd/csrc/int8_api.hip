@@ -4,8 +4,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <new>
-#include <vector>
 
 #include "int8.h"
 #include "lora_plan.h"
@@ -156,17 +154,27 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
                                    dt_of(w->dtype), (hipStream_t)stream);
 }
 
-// One layer of qlora_lora_grads_batch_int8: x restored, then the two contractions.
-static size_t grads_layer_ws(const qlora_lora_grads_int8& g, int r) {
-    if (g.M == 0) return 0;
-    return align256((size_t)g.M * g.K * 2) + align256(tn_ws_bytes(g.M, g.K, r)) + align256(tn_ws_bytes(g.M, g.N, r));
+// Tiles of one launch of the gradient kernel: the layers [i0, i0 + n) of a batch.
+static int64_t grads_tiles(const qlora_lora_grads_int8* layers, int n) {
+    int64_t t = 0;
+    for (int i = 0; i < n; ++i)
+        if (layers[i].M > 0) t += (layers[i].K + 127) / 128 + (layers[i].N + 127) / 128;
+    return t;
 }
 
 size_t qlora_lora_grads_batch_int8_workspace(const qlora_lora_grads_int8* layers, int count, int r) {
     if (!layers || count <= 0 || r < 1 || r > 128) return 0;
-    size_t total = 0;
     for (int i = 0; i < count; ++i)
-        if (!bad_sizes(layers[i].M, layers[i].N, layers[i].K, r)) total += grads_layer_ws(layers[i], r);
+        if (bad_sizes(layers[i].M, layers[i].N, layers[i].K, r)) return 0;
+    size_t total = 0;
+    for (int i0 = 0; i0 < count; i0 += kInt8GradLayers) {
+        const int n = std::min(kInt8GradLayers, count - i0);
+        const int64_t tiles = grads_tiles(layers + i0, n);
+        for (int i = i0; i < i0 + n; ++i) {
+            const qlora_lora_grads_int8& g = layers[i];
+            if (g.M > 0) total += plan_int8_grad(g.M, g.K, r, tiles).ws + plan_int8_grad(g.M, g.N, r, tiles).ws;
+        }
+    }
     return total;
 }
 
@@ -178,7 +186,9 @@ qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, in
     for (int i = 0; i < count; ++i) {  // every entry is checked before anything is launched
         const qlora_lora_grads_int8& g = layers[i];
         if (bad_sizes(g.M, g.N, g.K, r) || !g.dA || !g.dB) return QLORA_ERR_INVALID_ARG;
-        if (g.K % kBlock) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        // rows of at most 8 MB: the kernel counts what is left of a wave's rows, and the steps in
+        // flight past their end, in 32 signed bits
+        if (g.K % kBlock || g.K > (int64_t(1) << 22) || g.N > (int64_t(1) << 22)) return QLORA_ERR_UNSUPPORTED_SHAPE;
         if (!aligned16(g.dA) || !aligned16(g.dB)) return QLORA_ERR_MISALIGNED;
         if (g.M == 0) continue;
         if (!g.x || !g.x_scale || !g.t || !g.u || !g.dy) return QLORA_ERR_INVALID_ARG;
@@ -189,25 +199,28 @@ qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, in
     if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
-    const int dt = dt_of(dtype);
     size_t off = 0;
-    for (int i = 0; i < count; ++i) {
-        const qlora_lora_grads_int8& g = layers[i];
-        qlora_status st;
-        if (g.M == 0) {  // empty sums
-            if ((st = launch_fill(g.dA, g.K * r, 0.0f, s)) != QLORA_OK) return st;
-            if ((st = launch_fill(g.dB, (int64_t)r * g.N, 0.0f, s)) != QLORA_OK) return st;
-            continue;
+    qlora_status st;
+    for (int i0 = 0; i0 < count; i0 += kInt8GradLayers) {
+        const int n = std::min(kInt8GradLayers, count - i0);
+        const int64_t tiles = grads_tiles(layers + i0, n);
+        Int8GradDesc d[2 * kInt8GradLayers];
+        int m = 0;
+        for (int i = i0; i < i0 + n; ++i) {
+            const qlora_lora_grads_int8& g = layers[i];
+            if (g.M == 0) {  // empty sums
+                if ((st = launch_fill(g.dA, g.K * r, 0.0f, s)) != QLORA_OK) return st;
+                if ((st = launch_fill(g.dB, (int64_t)r * g.N, 0.0f, s)) != QLORA_OK) return st;
+                continue;
+            }
+            d[m] = Int8GradDesc{g.x, g.x_scale, g.u, g.dA, at(ws, off), (int)g.M, (int)g.K,
+                                plan_int8_grad(g.M, g.K, r, tiles)};
+            off += d[m++].plan.ws;
+            d[m] = Int8GradDesc{g.dy, nullptr, g.t, g.dB, at(ws, off), (int)g.M, (int)g.N,
+                                plan_int8_grad(g.M, g.N, r, tiles)};
+            off += d[m++].plan.ws;
         }
-        uint16_t* x16 = reinterpret_cast<uint16_t*>(at(ws, off));
-        off += align256((size_t)g.M * g.K * 2);
-        if ((st = launch_int8_dequantize(g.x, g.x_scale, g.M, g.K, dt, x16, s)) != QLORA_OK) return st;
-        TnDesc d[2];
-        d[0] = TnDesc{x16, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1};
-        off += align256(tn_ws_bytes(g.M, g.K, r));
-        d[1] = TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N};
-        off += align256(tn_ws_bytes(g.M, g.N, r));
-        if ((st = launch_tn_batch(d, 2, r, dt, s)) != QLORA_OK) return st;
+        if ((st = launch_int8_grads(d, m, r, dt_of(dtype), s)) != QLORA_OK) return st;
     }
     return QLORA_OK;
 }
