@@ -249,17 +249,30 @@ __device__ __forceinline__ void grad_body(const GradProb& pr, int r, int tile, i
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int j = 0; j < CW; ++j) tot[c][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < pr.splits - 1; ++s) {
-            const rsrc_t rs = buf_rsrc(reinterpret_cast<uint8_t*>(pr.part) + ((size_t)s * pr.tiles + tile) * kTile, kTile);
+        // several splits' tiles in flight at a time: each load comes from the device-coherent level
+        constexpr int kRound = CW == 4 ? 2 : 4;
+        const int last = pr.splits - 1;
+        for (int s = 0; s < last; s += kRound) {
+            u32x4_t g[kRound][4][CW];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int k = 0; k < kRound; ++k) {
+                const int from = min(s + k, last - 1);
+                const rsrc_t rs = buf_rsrc(reinterpret_cast<uint8_t*>(pr.part) + ((size_t)from * pr.tiles + tile) * kTile,
+                                           s + k < last ? kTile : 0u);   // past the last: zeros
 #pragma unroll
-                for (int j = 0; j < CW; ++j) {
-                    const f32x4_t v = __builtin_bit_cast(
-                        f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, poff(c, j), 0, kCoherent));
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) tot[c][j][e] += v[e];
-                }
+                    for (int j = 0; j < CW; ++j)
+                        g[k][c][j] = __builtin_amdgcn_raw_buffer_load_b128(rs, poff(c, j), 0, kCoherent);
+            }
+#pragma unroll
+            for (int k = 0; k < kRound; ++k)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tot[c][j][e] += __uint_as_float(g[k][c][j][e]);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -327,9 +340,12 @@ Int8GradPlan plan_int8_grad(int64_t M, int64_t D, int r, int64_t all_tiles) {
     p.tiles = (D + kGrCols - 1) / kGrCols;
     // a wave's rows (a quarter of a chunk) are addressed with 31 bits
     const int64_t most = std::min<int64_t>(kInt8GradChunk, (int64_t(1) << 30) / (2 * D) / 16 * 64);
-    const int64_t want = std::max<int64_t>((1024 + all_tiles - 1) / all_tiles, (M + most - 1) / most);
-    const int64_t s = std::max<int64_t>(1, std::min<int64_t>(want, (M + 63) / 64));
-    p.chunk = ((M + s - 1) / s + 63) / 64 * 64;
+    // One workgroup per CU is enough to stream, and a split costs a partial tile written and
+    // read again (32 KB at r = 64 against 128 bytes a row of codes): split only to fill the
+    // 256 CUs, and not below 256 rows.  M = 4096, K = N = 4096, r = 64: 4 splits 20.9 us, 2
+    // splits 28.6, 8 splits 25.1; M = 500, N = 11008: 1 split 10.4 us, 2 splits 11.5, 3 13.0.
+    const int64_t s = std::max<int64_t>((M + most - 1) / most, std::min<int64_t>(256 / all_tiles, M / 256));
+    p.chunk = ((M + std::max<int64_t>(s, 1) - 1) / std::max<int64_t>(s, 1) + 63) / 64 * 64;
     p.splits = (M + p.chunk - 1) / p.chunk;
     p.ws_tags = align256((size_t)(p.tiles * p.splits) * 8);
     p.ws = p.ws_tags + align256((size_t)((p.splits - 1) * p.tiles) * 4 * 4 * ranks_per_lane(r) * 64 * 16);
