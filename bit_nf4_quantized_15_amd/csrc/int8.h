@@ -25,6 +25,69 @@ __device__ __forceinline__ u32x2_t int8_values4(uint32_t b, float scale) {
     return u32x2_t{pack2<DT>(f0, f1), pack2<DT>(f2, f3)};
 }
 
+// ---- codes of a row.
+// With a = max|x| of the row, the code is the integer nearest to 127 x / a in exact
+// arithmetic, ties toward zero.  One fma decides it: fma(x, inv, 1.5 * 2^23) with
+// inv = fl(127/a) (1 - 2^-21), whose low byte is the rounded integer in two's
+// complement.  inv is below 127/a by a relative 2^-21 +- 2^-23.  A real quotient that is
+// no tie lies at least 1/(254 * 2047) > 2^-19 (fp16; bf16 1/(254 * 255) > 2^-16) of itself
+// away from any half-integer, because 254 x and (2j + 1) a differ by a whole unit of
+// x's mantissa; so the small cut moves no such quotient across a half, and it moves every
+// tie to just below its half: toward zero.
+template <int DT>
+constexpr uint32_t kInfBits = DT == kDtF16 ? 0x7C00u : 0x7F80u;
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// The larger magnitude bits of two packed pairs (as integers: NaN above infinity above finite).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
+    const u16x2_t a = __builtin_bit_cast(u16x2_t, m), b = __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+}
+
+// What a row's codes need: one multiplier (and a power of two for rows of tiny values,
+// whose reciprocal would overflow).
+struct RowScale {
+    float inv, pre, scale;
+    bool bad;
+};
+template <int DT>
+__device__ __forceinline__ RowScale row_scale(uint32_t abits) {
+    RowScale r;
+    r.bad = abits >= kInfBits<DT>;
+    const float a = h16_to_f32<DT>(abits);
+    r.scale = r.bad ? __builtin_nanf("") : a / 127.0f;
+    r.pre = DT == kDtBf16 && a < 0x1p-100f ? 0x1p100f : 1.0f;   // exact: bf16 values are multiples of 2^-133
+    r.inv = abits == 0u || r.bad ? 0.0f : 127.0f / (a * r.pre) * (1.0f - 0x1p-21f);
+    return r;
+}
+
+// Codes of the 8 values of v; zero rows and rows that are not finite give 0 (inv = 0, and
+// for the latter the value is replaced before the fma).
+template <int DT>
+__device__ __forceinline__ u32x2_t codes8(u32x4_t v, const RowScale& r) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = r.bad ? 0u : v[i];
+        float lo = h16_to_f32<DT>(w & 0xFFFFu), hi = h16_to_f32<DT>(w >> 16);
+        if (DT == kDtBf16) {
+            lo *= r.pre;
+            hi *= r.pre;
+        }
+        b[2 * i] = __float_as_uint(__builtin_fmaf(lo, r.inv, 12582912.0f));
+        b[2 * i + 1] = __float_as_uint(__builtin_fmaf(hi, r.inv, 12582912.0f));
+    }
+    u32x2_t o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t p01 = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0400u);
+        const uint32_t p23 = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000C0Cu);
+        o[i] = p01 | p23;
+    }
+    return o;
+}
+
 qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scale, int dt,
                                   hipStream_t s);
 qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int dt,
@@ -33,6 +96,17 @@ qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int
 qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                   const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
                                   hipStream_t s);
+// The forward for up to kInt8GemvMaxM tokens in one launch.  x 16-bit, quantized by the kernel
+// (xq null; int8_gemv_quantizes says for which sizes), or its codes xq, sx; t given, or made
+// from x (then not null) and A in the launch, with int8_gemv_workspace(r) bytes of workspace
+// that need no clearing, and stored to t_out (nullable).
+constexpr int kInt8GemvMaxM = 16;
+bool int8_gemv_supported(int64_t M, int64_t N, int64_t K, int r);
+bool int8_gemv_quantizes(int64_t M, int64_t K);
+size_t int8_gemv_workspace(int r);
+qlora_status launch_int8_gemv(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                              const uint16_t* t, const uint16_t* A, const uint16_t* B, float scale, uint16_t* y,
+                              uint16_t* t_out, void* ws, int M, int N, int K, int r, int dt, hipStream_t s);
 // dx = RNE_16(dy W_16 + u A^T); r == 0: no u A^T
 qlora_status launch_int8_gemm_bwd_dx(const uint16_t* dy, const int8_t* wq, const float* sw, const uint16_t* u,
                                      const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt,

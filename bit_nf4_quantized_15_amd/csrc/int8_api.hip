@@ -36,8 +36,14 @@ inline bool bad_sizes(int64_t M, int64_t N, int64_t K, int r) {
 struct FwdWs {
     size_t codes, scale, tbuf, part, total;  // x in 8 bits; t when the caller keeps none; split sums of t
 };
-inline FwdWs fwd_ws(int64_t M, int64_t K, int r) {
+inline FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     FwdWs w{};
+    if (int8_gemv_supported(M, N, K, r)) {   // one launch; codes only where it does not make them itself
+        w.scale = align256((size_t)M * K);
+        w.part = w.scale + align256((size_t)M * 4);
+        w.total = w.part + int8_gemv_workspace(r);
+        return w;
+    }
     w.codes = 0;
     w.scale = align256((size_t)M * K);
     w.tbuf = w.scale + align256((size_t)M * 4);
@@ -71,7 +77,7 @@ qlora_status qlora_int8_dequantize(const qlora_int8* q, uint16_t* out, void* str
 
 size_t qlora_int8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r) {
     if (bad_sizes(M, N, K, r) || M == 0 || K % kBlock) return 0;
-    return fwd_ws(M, K, r).total;
+    return fwd_ws(M, N, K, r).total;
 }
 
 qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64_t M, const uint16_t* A,
@@ -90,7 +96,7 @@ qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64
     if (!x || !y || (r && (!A || !B)) || (!r && (A || B || t_out))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(y) || !aligned16(A) || !aligned16(B) || !aligned16(t_out))
         return QLORA_ERR_MISALIGNED;
-    const FwdWs W = fwd_ws(M, K, r);
+    const FwdWs W = fwd_ws(M, N, K, r);
     if (!ws || ws_bytes < W.total) return QLORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
@@ -98,7 +104,12 @@ qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64
     int8_t* xq = x_keep ? x_keep->codes : reinterpret_cast<int8_t*>(at(ws, W.codes));
     float* sx = x_keep ? x_keep->scale : reinterpret_cast<float*>(at(ws, W.scale));
     uint16_t* t = t_out ? t_out : reinterpret_cast<uint16_t*>(at(ws, W.tbuf));
-    if ((st = launch_int8_quantize(x, M, K, xq, sx, dt, s)) != QLORA_OK) return st;
+    const bool decode = int8_gemv_supported(M, N, K, r);
+    if (decode && !x_keep && int8_gemv_quantizes(M, K)) xq = nullptr;
+    else if ((st = launch_int8_quantize(x, M, K, xq, sx, dt, s)) != QLORA_OK) return st;
+    if (decode)
+        return launch_int8_gemv(x, xq, sx, w->codes, w->scale, nullptr, A, B, r ? alpha / (float)r : 0.0f, y, t_out,
+                                at(ws, W.part), (int)M, (int)N, (int)K, r, dt, s);
     if (r && (st = launch_nt(x, A, true, at(ws, W.part), t, alpha / (float)r, (int)M, (int)K, r, dt, s)) != QLORA_OK)
         return st;
     return launch_int8_gemm_fwd(xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, dt, s);
@@ -113,6 +124,9 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
     if (x->rows == 0) return QLORA_OK;
     if (!y || (r && (!t || !B)) || (!r && (t || B))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(y) || !aligned16(t) || !aligned16(B)) return QLORA_ERR_MISALIGNED;
+    if (int8_gemv_supported(x->rows, w->rows, w->cols, r))
+        return launch_int8_gemv(nullptr, x->codes, x->scale, w->codes, w->scale, t, nullptr, B, 0.0f, y, nullptr, nullptr,
+                                (int)x->rows, (int)w->rows, (int)w->cols, r, dt_of(w->dtype), (hipStream_t)stream);
     return launch_int8_gemm_fwd(x->codes, x->scale, w->codes, w->scale, t, B, y, (int)x->rows, (int)w->rows,
                                 (int)w->cols, r, dt_of(w->dtype), (hipStream_t)stream);
 }

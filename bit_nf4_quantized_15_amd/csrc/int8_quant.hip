@@ -1,74 +1,12 @@
 // int8 codes with one fp32 scale per row, and the 16-bit values back from them
 // ("bitsandbytes deep dive", section 4: absmax int8, one scale per row).
-//
-// With a = max|x| of the row, the code is the integer nearest to 127 x / a in exact
-// arithmetic, ties toward zero.  One fma decides it: fma(x, inv, 1.5 * 2^23) with
-// inv = fl(127/a) (1 - 2^-21), whose low byte is the rounded integer in two's
-// complement.  inv is below 127/a by a relative 2^-21 +- 2^-23.  A real quotient that is
-// no tie lies at least 1/(254 * 2047) > 2^-19 (fp16; bf16 1/(254 * 255) > 2^-16) of itself
-// away from any half-integer, because 254 x and (2j + 1) a differ by a whole unit of
-// x's mantissa; so the small cut moves no such quotient across a half, and it moves every
-// tie to just below its half: toward zero.
+// The rounding of a code is decided as int8.h shows.
 #include "int8.h"
 
 namespace qlora {
 namespace {
 
 constexpr int kQT = 256;   // lanes per row
-
-template <int DT>
-constexpr uint32_t kInfBits = DT == kDtF16 ? 0x7C00u : 0x7F80u;
-
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-
-// The larger magnitude bits of two packed pairs (as integers: NaN above infinity above finite).
-__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
-    const u16x2_t a = __builtin_bit_cast(u16x2_t, m), b = __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu);
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
-}
-
-// What a row's codes need: one multiplier (and a power of two for rows of tiny values,
-// whose reciprocal would overflow).
-struct RowScale {
-    float inv, pre, scale;
-    bool bad;
-};
-template <int DT>
-__device__ __forceinline__ RowScale row_scale(uint32_t abits) {
-    RowScale r;
-    r.bad = abits >= kInfBits<DT>;
-    const float a = h16_to_f32<DT>(abits);
-    r.scale = r.bad ? __builtin_nanf("") : a / 127.0f;
-    r.pre = DT == kDtBf16 && a < 0x1p-100f ? 0x1p100f : 1.0f;   // exact: bf16 values are multiples of 2^-133
-    r.inv = abits == 0u || r.bad ? 0.0f : 127.0f / (a * r.pre) * (1.0f - 0x1p-21f);
-    return r;
-}
-
-// Codes of the 8 values of v; zero rows and rows that are not finite give 0 (inv = 0, and
-// for the latter the value is replaced before the fma).
-template <int DT>
-__device__ __forceinline__ u32x2_t codes8(u32x4_t v, const RowScale& r) {
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = r.bad ? 0u : v[i];
-        float lo = h16_to_f32<DT>(w & 0xFFFFu), hi = h16_to_f32<DT>(w >> 16);
-        if (DT == kDtBf16) {
-            lo *= r.pre;
-            hi *= r.pre;
-        }
-        b[2 * i] = __float_as_uint(__builtin_fmaf(lo, r.inv, 12582912.0f));
-        b[2 * i + 1] = __float_as_uint(__builtin_fmaf(hi, r.inv, 12582912.0f));
-    }
-    u32x2_t o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t p01 = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0400u);
-        const uint32_t p23 = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000C0Cu);
-        o[i] = p01 | p23;
-    }
-    return o;
-}
 
 // One workgroup per row, two passes over it.
 template <int DT>
