@@ -6,34 +6,78 @@
 namespace qlora {
 namespace {
 
-constexpr int kQT = 256;   // lanes per row
+constexpr int kQT = 256;   // lanes per workgroup
 
-// One workgroup per row, two passes over it.
-template <int DT>
-__global__ __launch_bounds__(kQT) void int8_quantize_kernel(const uint16_t* __restrict__ x, int cols,
-                                                            int8_t* __restrict__ codes, float* __restrict__ scale) {
-    __shared__ uint32_t red[kQT / 64];
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
-    const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + row * cols);
-    u32x2_t* cr = reinterpret_cast<u32x2_t*>(codes + row * cols);
-    const int nch = cols >> 3;
-    uint32_t m = 0;
-    for (int c = tid; c < nch; c += kQT) {
-        const u32x4_t v = xr[c];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max_abs2(m, v[i]);
-    }
+// A row's largest magnitude bits over the W waves that share it.
+template <int W>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
     uint32_t a = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
     for (int d = 32; d; d >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, d));
-    if ((tid & 63) == 0) red[tid >> 6] = a;
-    __syncthreads();
+    if (W > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) red[wave] = a;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQT / 64; ++w) a = max(a, red[w]);
-    const RowScale r = row_scale<DT>(a);
-    if (tid == 0) scale[row] = r.scale;
-    for (int c = tid; c < nch; c += kQT) cr[c] = codes8<DT>(xr[c], r);
+        for (int w = 0; w < W; ++w) a = max(a, red[w]);
+    }
+    return a;
+}
+
+// Rows of up to 512 W C values: W waves hold a row in registers, C 16-byte chunks per lane,
+// so x is read once (HBM bound: one pass in, half of it out).
+template <int W, int C, int DT>
+__global__ __launch_bounds__(kQT) void int8_quantize_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
+                                                            int8_t* __restrict__ codes, float* __restrict__ scale) {
+    constexpr int kPer = kQT / 64 / W;   // rows per workgroup
+    __shared__ uint32_t red[2][kQT / 64];
+    const int lane = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W), nch = cols >> 3;
+    int turn = 0;
+    for (int64_t base = (int64_t)blockIdx.x * kPer; base < rows; base += (int64_t)gridDim.x * kPer, turn ^= 1) {
+        const int64_t row = base + sub;
+        const bool on = row < rows;
+        const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (on ? row : rows - 1) * cols);
+        u32x4_t v[C];
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = xr[min(lane + 64 * W * e, nch - 1)];   // (the last chunk again)
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < C; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max_abs2(m, v[e][i]);
+        // two buffers: a wave may be a row ahead of one that still reads
+        const RowScale r = row_scale<DT>(row_max<W>(m, red[turn]));
+        if (!on) continue;
+        if (lane == 0) scale[row] = r.scale;
+        u32x2_t* cr = reinterpret_cast<u32x2_t*>(codes + row * cols);
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+            const int c = lane + 64 * W * e;
+            if (c < nch) cr[c] = codes8<DT>(v[e], r);
+        }
+    }
+}
+
+// Longer rows: one workgroup per row, two passes over it.
+template <int DT>
+__global__ __launch_bounds__(kQT) void int8_quantize_long_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
+                                                                 int8_t* __restrict__ codes, float* __restrict__ scale) {
+    __shared__ uint32_t red[2][kQT / 64];
+    const int tid = threadIdx.x, nch = cols >> 3;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + row * cols);
+        u32x2_t* cr = reinterpret_cast<u32x2_t*>(codes + row * cols);
+        uint32_t m = 0;
+        for (int c = tid; c < nch; c += kQT) {
+            const u32x4_t v = xr[c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max_abs2(m, v[i]);
+        }
+        const RowScale r = row_scale<DT>(row_max<kQT / 64>(m, red[turn]));
+        if (tid == 0) scale[row] = r.scale;
+        for (int c = tid; c < nch; c += kQT) cr[c] = codes8<DT>(xr[c], r);
+    }
 }
 
 // 16 codes per lane; `base` counts 16-code chunks of the whole tensor.
@@ -71,9 +115,24 @@ __global__ __launch_bounds__(256) void int8_dequantize_kernel(const int8_t* __re
 
 qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scale, int dt,
                                   hipStream_t s) {
+    const int nch = (int)(cols >> 3);
+    const unsigned grid4 = (unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20);   // four rows per workgroup
+    const unsigned grid1 = (unsigned)std::min<int64_t>(rows, 1 << 20);
     with_dt(dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
-        hipLaunchKernelGGL(int8_quantize_kernel<DT>, dim3((unsigned)rows), dim3(kQT), 0, s, x, (int)cols, codes, scale);
+#define QL_Q(W, C) \
+    hipLaunchKernelGGL((int8_quantize_kernel<W, C, DT>), dim3(W == 1 ? grid4 : grid1), dim3(kQT), 0, s, x, rows, \
+                       (int)cols, codes, scale)
+        if (nch <= 64) QL_Q(1, 1);
+        else if (nch <= 256) QL_Q(1, 4);
+        else if (nch <= 512) QL_Q(4, 2);
+        else if (nch <= 1024) QL_Q(4, 4);
+        else if (nch <= 2048) QL_Q(4, 8);
+        else if (nch <= 4096) QL_Q(4, 16);
+        else
+            hipLaunchKernelGGL(int8_quantize_long_kernel<DT>, dim3(grid1), dim3(kQT), 0, s, x, rows, (int)cols, codes,
+                               scale);
+#undef QL_Q
     });
     return launch_status();
 }

@@ -164,7 +164,9 @@ def _check(status, where):
 
 
 def _stream():
-    return c_vp(torch.cuda.current_stream().cuda_stream)
+    """The current stream's handle.  Read directly: building torch's stream object takes longer (2.9 us) than
+    checking the arguments of a call."""
+    return c_vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t):
@@ -553,10 +555,12 @@ def pooled_bwd(w, x, A, B, alpha, g, dy, t=None, need_dx=True, dx=None, dA=None,
     return dx, dA, dB
 
 
-def _on_current_device(t, name):
-    """The int8 calls run on the current stream of the current device: a tensor of another device is refused."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _stream_of(t, name):
+    """The stream of an int8 call: the current one of the current device, where its tensors have to be."""
+    cur = torch.cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
+    return c_vp(torch._C._cuda_getCurrentRawStream(cur))
 
 
 class Int8Tensor:
@@ -578,8 +582,13 @@ class Int8Tensor:
 
     @classmethod
     def empty(cls, rows, cols, device="cuda", dtype=torch.bfloat16):
-        return cls(_empty((rows, cols), dtype=torch.int8, device=device),
-                   _empty((rows,), dtype=torch.float32, device=device), dtype)
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        q = cls.__new__(cls)      # (made here: nothing to check)
+        q.codes = _empty((rows, cols), dtype=torch.int8, device=device)
+        q.scale = _empty((rows,), dtype=torch.float32, device=device)
+        q.dtype, q.rows, q.cols = dtype, rows, cols
+        return q
 
     def state(self):
         return Int8State(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, DTYPES[self.dtype])
@@ -591,8 +600,7 @@ def int8_quantize(x, out=None):
     rows, cols = x.shape
     q = Int8Tensor.empty(rows, cols, x.device, x.dtype) if out is None else out
     _dev(x, q.dtype, "x", (q.rows, q.cols))
-    _on_current_device(x, "x")
-    _check(lib.qlora_int8_quantize(_ptr(x), ctypes.byref(q.state()), _stream()), "qlora_int8_quantize")
+    _check(lib.qlora_int8_quantize(_ptr(x), ctypes.byref(q.state()), _stream_of(x, "x")), "qlora_int8_quantize")
     return q
 
 
@@ -600,8 +608,8 @@ def int8_dequantize(q, out=None):
     """The 16-bit [rows, cols] tensor that the codes stand for (qlora_int8_dequantize)."""
     o = _empty((q.rows, q.cols), dtype=q.dtype, device=q.codes.device) if out is None else out
     _dev(o, q.dtype, "out", (q.rows, q.cols))
-    _on_current_device(q.codes, "q")
-    _check(lib.qlora_int8_dequantize(ctypes.byref(q.state()), _ptr(o), _stream()), "qlora_int8_dequantize")
+    _check(lib.qlora_int8_dequantize(ctypes.byref(q.state()), _ptr(o), _stream_of(q.codes, "q")),
+           "qlora_int8_dequantize")
     return o
 
 
@@ -627,7 +635,7 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     r = _int8_branch(w, A, B)
     dev = x.device
     _dev(x, w.dtype, "x", (M, w.cols))
-    _on_current_device(x, "x")
+    stream = _stream_of(x, "x")
     y = _empty((M, w.rows), dtype=w.dtype, device=dev) if y is None else _dev(y, w.dtype, "y", (M, w.rows))
     if r == 0:
         if t is not None:
@@ -641,7 +649,7 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     wsb, wsn = _ws(int(lib.qlora_int8_fwd_workspace(M, w.rows, w.cols, r)), dev, ws)
     _check(lib.qlora_int8_linear_fwd(ctypes.byref(w.state()), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(y),
                                      _ptr(t), None if keep is None else ctypes.byref(keep.state()), _ptr(wsb), wsn,
-                                     _stream()), "qlora_int8_linear_fwd")
+                                     stream), "qlora_int8_linear_fwd")
     return y, t
 
 
@@ -656,11 +664,11 @@ def int8_gemm_fwd(w, x, t=None, B=None, y=None):
     if t is not None:
         _dev(t, w.dtype, "t", (x.rows, r))
         _dev(B, w.dtype, "B", (r, w.rows))
-    _on_current_device(x.codes, "x")
+    stream = _stream_of(x.codes, "x")
     y = _empty((x.rows, w.rows), dtype=w.dtype, device=x.codes.device) if y is None else \
         _dev(y, w.dtype, "y", (x.rows, w.rows))
     _check(lib.qlora_int8_gemm_fwd(ctypes.byref(w.state()), ctypes.byref(x.state()), _ptr(t), _ptr(B), r, _ptr(y),
-                                   _stream()), "qlora_int8_gemm_fwd")
+                                   stream), "qlora_int8_gemm_fwd")
     return y
 
 
@@ -671,7 +679,7 @@ def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
     r = _int8_branch(w, A, B)
     dev = dy.device
     _dev(dy, w.dtype, "dy", (M, w.rows))
-    _on_current_device(dy, "dy")
+    stream = _stream_of(dy, "dy")
     if r:
         u = _empty((M, r), dtype=w.dtype, device=dev) if u is None else _dev(u, w.dtype, "u", (M, r))
     elif u is not None:
@@ -679,7 +687,7 @@ def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
     dx = _empty((M, w.cols), dtype=w.dtype, device=dev) if dx is None else _dev(dx, w.dtype, "dx", (M, w.cols))
     wsb, wsn = _ws(int(lib.qlora_int8_linear_bwd_dx_workspace(M, w.rows, w.cols, r)), dev, ws)
     _check(lib.qlora_int8_linear_bwd_dx(ctypes.byref(w.state()), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(dy),
-                                        _ptr(u), _ptr(dx), _ptr(wsb), wsn, _stream()), "qlora_int8_linear_bwd_dx")
+                                        _ptr(u), _ptr(dx), _ptr(wsb), wsn, stream), "qlora_int8_linear_bwd_dx")
     return u, dx
 
 
@@ -693,11 +701,11 @@ def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None):
     if u is not None:
         _dev(u, w.dtype, "u", (M, r))
         _dev(A, w.dtype, "A", (w.cols, r))
-    _on_current_device(dy, "dy")
+    stream = _stream_of(dy, "dy")
     dx = _empty((M, w.cols), dtype=w.dtype, device=dy.device) if dx is None else \
         _dev(dx, w.dtype, "dx", (M, w.cols))
     _check(lib.qlora_int8_gemm_bwd_dx(ctypes.byref(w.state()), _ptr(dy), M, _ptr(u), _ptr(A), r, _ptr(dx),
-                                      _stream()), "qlora_int8_gemm_bwd_dx")
+                                      stream), "qlora_int8_gemm_bwd_dx")
     return dx
 
 
@@ -723,7 +731,7 @@ def lora_grads_batch_int8(layers, dA=None, dB=None, ws=None):
         _dev(t, dt, "t", (M, r))
         _dev(u, dt, "u", (M, r))
         _dev(dy, dt, "dy", (M, N))
-        _on_current_device(x.codes, "x")
+        stream = _stream_of(x.codes, "x")
         dev = dy.device
         dA[i] = _empty((K, r), dtype=torch.float32, device=dev) if dA[i] is None else \
             _dev(dA[i], torch.float32, "dA", (K, r))
@@ -732,7 +740,7 @@ def lora_grads_batch_int8(layers, dA=None, dB=None, ws=None):
         descs[i] = LoraGradsInt8(x.codes.data_ptr(), x.scale.data_ptr(), t.data_ptr(), u.data_ptr(), dy.data_ptr(),
                                  dA[i].data_ptr(), dB[i].data_ptr(), M, N, K)
     wsb, wsn = _ws(int(lib.qlora_lora_grads_batch_int8_workspace(descs, n, r)), dev, ws)
-    _check(lib.qlora_lora_grads_batch_int8(descs, n, r, DTYPES[dt], _ptr(wsb), wsn, _stream()),
+    _check(lib.qlora_lora_grads_batch_int8(descs, n, r, DTYPES[dt], _ptr(wsb), wsn, stream),
            "qlora_lora_grads_batch_int8")
     return dA, dB
 
