@@ -92,10 +92,12 @@ qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols,
                                   hipStream_t s);
 qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int dt,
                                     uint16_t* out, hipStream_t s);
-// y = RNE_16(sx sw (xq wq^T) + t B); r == 0: no t B
+// y = RNE_16(sx sw (xq wq^T) + t B); r == 0: no t B.  ws (nullable): int8_gemm_fwd_workspace
+// bytes that need no clearing, with which small products split their reduction.
+size_t int8_gemm_fwd_workspace(int64_t M, int64_t N, int64_t K);
 qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                   const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
-                                  hipStream_t s);
+                                  void* ws, hipStream_t s);
 // The forward for up to kInt8GemvMaxM tokens in one launch.  x 16-bit, quantized by the kernel
 // (xq null; int8_gemv_quantizes says for which sizes), or its codes xq, sx; t given, or made
 // from x (then not null) and A in the launch, with int8_gemv_workspace(r) bytes of workspace

@@ -34,7 +34,7 @@ inline bool bad_sizes(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 struct FwdWs {
-    size_t codes, scale, tbuf, part, total;  // x in 8 bits; t when the caller keeps none; split sums of t
+    size_t codes, scale, tbuf, part, gemm, total;  // x in 8 bits; t when the caller keeps none; split sums of t, of y
 };
 inline FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     FwdWs w{};
@@ -48,7 +48,8 @@ inline FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     w.scale = align256((size_t)M * K);
     w.tbuf = w.scale + align256((size_t)M * 4);
     w.part = w.tbuf + align256((size_t)M * r * 2);
-    w.total = w.part + (r ? align256(nt_ws_bytes(M, K, r)) : 0);
+    w.gemm = w.part + (r ? align256(nt_ws_bytes(M, K, r)) : 0);
+    w.total = w.gemm + int8_gemm_fwd_workspace(M, N, K);
     return w;
 }
 
@@ -112,7 +113,8 @@ qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64
                                 at(ws, W.part), (int)M, (int)N, (int)K, r, dt, s);
     if (r && (st = launch_nt(x, A, true, at(ws, W.part), t, alpha / (float)r, (int)M, (int)K, r, dt, s)) != QLORA_OK)
         return st;
-    return launch_int8_gemm_fwd(xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, dt, s);
+    return launch_int8_gemm_fwd(xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, dt,
+                                at(ws, W.gemm), s);
 }
 
 qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const uint16_t* t, const uint16_t* B,
@@ -128,7 +130,7 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
         return launch_int8_gemv(nullptr, x->codes, x->scale, w->codes, w->scale, t, nullptr, B, 0.0f, y, nullptr, nullptr,
                                 (int)x->rows, (int)w->rows, (int)w->cols, r, dt_of(w->dtype), (hipStream_t)stream);
     return launch_int8_gemm_fwd(x->codes, x->scale, w->codes, w->scale, t, B, y, (int)x->rows, (int)w->rows,
-                                (int)w->cols, r, dt_of(w->dtype), (hipStream_t)stream);
+                                (int)w->cols, r, dt_of(w->dtype), nullptr, (hipStream_t)stream);
 }
 
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r) {

@@ -217,27 +217,29 @@ __global__ __launch_bounds__(kThreads, MT* NT >= 16 ? 1 : 2) void int8_gemm_dx_k
                                                    urs, j < r ? (uint32_t)(row * r + j) * 2u : 0x80000000u, 0, 0));
         return m0 + row < M && j < r ? load8(u + (int64_t)(m0 + row) * r + j, j, r) : u32x4_t{0u, 0u, 0u, 0u};
     };
+    load(s0, 0);
+    put_dy(s0);
+    load(s1, 1);
+    put_dy(s1);
     u32x4_t av[NT][4];
     if (r)
 #pragma unroll
         for (int e = 0; e < NT; ++e)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) av[e][kk] = load_a(e, kk);
-
+    __builtin_amdgcn_sched_barrier(0);
+    load(s2, 2);
+    put_dy(s2);
+    // zeros from the matrix unit while the first tiles are on their way (256 register writes,
+    // and the compiler's copies of them, took a microsecond)
     f32x16_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int e = 0; e < NT; ++e)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][e][v] = 0.0f;
-
-    load(s0, 0);
-    put_dy(s0);
-    load(s1, 1);
-    put_dy(s1);
-    load(s2, 2);
-    put_dy(s2);
+        for (int e = 0; e < NT; ++e) {
+            const u32x4_t z = {0u, 0u, 0u, 0u};
+            acc[i][e] = mfma16<DT>(z, z, f32x16_t{});
+        }
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");   // tiles 0 and 1 have landed
     u32x4_t da[2][MT], wb[2][NT];
     Codes q[2];
@@ -291,17 +293,29 @@ __global__ __launch_bounds__(kThreads, MT* NT >= 16 ? 1 : 2) void int8_gemm_dx_k
     // Lane (h, l32): token l32, columns 32 e + 8 v4 + 4 h + 0..3 of the wave's.
     constexpr int kRow = 2 * kBN, kCh = kBN / 8, kMask = (kCh < 16 ? kCh : 16) - 1;
     static_assert(32 * kRow <= kSlot, "32 output rows fit a slot");
+    const rsrc_t xrs = buf_rsrc(dx + (int64_t)m0 * K, (uint64_t)min(M - m0, kBM) * K * 2);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         if constexpr (MT * NT >= 16)
 #pragma unroll
             for (int e = 0; e < NT; ++e) asm volatile("" : "+a"(acc[i][e]));
-        for (int kk = 0; 16 * kk < r; ++kk) {
-            const u32x4_t uv = load_u(i, kk);
+        if (r) {   // (ranks past r are zero: 32 at a time, so that the sums keep their registers)
+            auto rank16 = [&](const u32x4_t (&a)[NT], u32x4_t uv) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 0; e < NT; ++e) {
-                const u32x4_t a = kk == 0 ? av[e][0] : kk == 1 ? av[e][1] : kk == 2 ? av[e][2] : kk == 3 ? av[e][3] : load_a(e, kk);
-                acc[i][e] = mfma16<DT>(a, uv, acc[i][e]);
+                for (int e = 0; e < NT; ++e) acc[i][e] = mfma16<DT>(a[e], uv, acc[i][e]);
+            };
+            u32x4_t a[NT];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk == 2 && r <= 32) break;
+#pragma unroll
+                for (int e = 0; e < NT; ++e) a[e] = av[e][kk];
+                rank16(a, load_u(i, kk));
+            }
+            for (int kk = 4; 16 * kk < r; ++kk) {
+#pragma unroll
+                for (int e = 0; e < NT; ++e) a[e] = load_a(e, kk);
+                rank16(a, load_u(i, kk));
             }
         }
         uint8_t* const slot = (i & 1) ? s1 : s0;
@@ -318,9 +332,11 @@ __global__ __launch_bounds__(kThreads, MT* NT >= 16 ? 1 : 2) void int8_gemm_dx_k
 #pragma unroll
         for (int p = 0; p < 32 * kCh / kThreads; ++p) {
             const int c = tid + kThreads * p, cc = c % kCh, rr = c / kCh;
-            const int m = m0 + 32 * i + rr, k = k0 + 8 * cc;
+            const int row = 32 * i + rr, k = k0 + 8 * cc;
             const u32x4_t v = *reinterpret_cast<const u32x4_t*>(slot + rr * kRow + 16 * (cc ^ (rr & kMask)));
-            if (m < M && k < K) *reinterpret_cast<u32x4_t*>(dx + (int64_t)m * K + k) = v;
+            // rows past M lie past the buffer and are dropped, as are columns past K
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, xrs, k < K ? ((uint32_t)row * (uint32_t)K + (uint32_t)k) * 2u : 0x80000000u, 0, 0);
         }
     }
 }
@@ -332,7 +348,7 @@ qlora_status run(const uint16_t* dy, const int8_t* wq, const float* sw, const ui
     const int tm = (int)(((int64_t)M + kBM - 1) / kBM), tn = (int)(((int64_t)K + kBN - 1) / kBN), gm = 4;
     const int64_t total = (int64_t)tm * tn;
     if (total * kThreads >= (int64_t(1) << 32) || (int64_t)gm * tn >= (int64_t(1) << 31) ||
-        (int64_t)kStep * K >= (int64_t(1) << 31))
+        (int64_t)kBM * K * 2 >= (int64_t(1) << 31))
         return QLORA_ERR_UNSUPPORTED_SHAPE;
     // direct loads of dy: whole 16-byte chunks, a panel's offsets within a buffer's 31 bits
     const bool dyv = N % 8 == 0 && (int64_t)kBM * N * 2 < (int64_t(1) << 31);

@@ -16,7 +16,11 @@
 // consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.  t, the
 // first 64 rows of B and the scales are fetched before the main loop into registers that it
 // has no use for, and the epilogue goes 32 tokens at a time (scale, t B, round, store).
+#include <cstdlib>
+
 #include "int8.h"
+#include "lora_plan.h"
+#include "split_sync.h"
 
 namespace qlora {
 
@@ -77,6 +81,9 @@ __device__ __forceinline__ uint32_t tile_byte(int row, int c) {
 // CUs at a time) then form a block of gm x 32 / gm that shares panels in the XCD's L2.
 struct TileMap {
     int tm, tn, gm;
+    int splits, per;      // the reduction in `splits` parts of `per` steps
+    uint64_t* tags;       // [tile][split]
+    uint8_t* part;        // [split][tile]: the int32 sums of every part but the last
 };
 __device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int& nt) {
     const int total = tp.tm * tp.tn, xcd = bid & 7, idx = bid >> 3, per = total >> 3, rem = total & 7;
@@ -88,8 +95,10 @@ __device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int
 
 // NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs.  VEC: r % 8 == 0 and
 // N % 8 == 0, so t, B and y are accessed 16 bytes at a time.
-template <int NWM, int NWN, int MT, int NT, bool VEC, int DT>
-__global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gemm_fwd_kernel(
+// LORA: r > 0.  SPLIT: the reduction is split over workgroups; the last part's adds the others' int32 sums
+// (exact, so y does not depend on the split).
+template <int NWM, int NWN, int MT, int NT, bool SPLIT, bool LORA, bool VEC, int DT>
+__global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gemm_fwd_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ sx, const int8_t* __restrict__ wq,
     const float* __restrict__ sw, const uint16_t* __restrict__ t, const uint16_t* __restrict__ B,
     uint16_t* __restrict__ y, int M, int N, int K, int r, TileMap tp) {
@@ -106,29 +115,38 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % NWM, wn = wave / NWM;
+    const int tiles = tp.tm * tp.tn, split = SPLIT ? (int)blockIdx.x / tiles : 0;
     int mt, nt;
-    tile_of(tp, blockIdx.x, mt, nt);
+    tile_of(tp, (int)blockIdx.x - split * tiles, mt, nt);
     const int m0 = mt * kBM, n0 = nt * kBN;
-    const int NS = K / kStep;
+    const int s_first = SPLIT ? split * tp.per : 0, NS = SPLIT ? min(tp.per, K / kStep - s_first) : K / kStep;
 
     // panels as buffers: rows past the end read as zero (the range check covers voffset)
-    const i32x4_t xrs = buffer_rsrc(xq + (int64_t)m0 * K, (uint32_t)min(M - m0, kBM) * (uint32_t)K);
-    const i32x4_t wrs = buffer_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(N - n0, kBN) * (uint32_t)K);
+    const uint32_t k_first = (uint32_t)(s_first * kStep);
+    const i32x4_t xrs = buffer_rsrc(xq + (int64_t)m0 * K + k_first, (uint32_t)min(M - m0, kBM) * (uint32_t)K - k_first);
+    const i32x4_t wrs = buffer_rsrc(wq + (int64_t)n0 * K + k_first, (uint32_t)min(N - n0, kBN) * (uint32_t)K - k_first);
     // a wave load fills 16 rows of 64 bytes; lane: row lane / 4, LDS chunk lane % 4
     const int lrow = lane >> 2, lch = (lane & 3) ^ ((lrow >> 2) & 3);
     const uint32_t voff = (uint32_t)(16 * wave + lrow) * (uint32_t)K + 16u * (uint32_t)lch;
-    auto load = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
-        i32x4_t xr = xrs, wr = wrs;
-        xr[2] = ks < NS ? xr[2] : 0;   // steps past K read as zero and move nothing
-        wr[2] = ks < NS ? wr[2] : 0;
+    auto load_x = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
+        i32x4_t rs = xrs;
+        rs[2] = ks < NS ? rs[2] : 0;   // steps past K read as zero and move nothing
 #pragma unroll
         for (int j = 0; j < kXL; ++j)
-            raw_buffer_load_lds(xr, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
+            raw_buffer_load_lds(rs, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
                                 (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+    };
+    auto load_w = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
+        i32x4_t rs = wrs;
+        rs[2] = ks < NS ? rs[2] : 0;
 #pragma unroll
         for (int j = 0; j < kWL; ++j)
-            raw_buffer_load_lds(wr, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
+            raw_buffer_load_lds(rs, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
                                 (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+    };
+    auto load = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
+        load_x(slot, ks);
+        load_w(slot, ks);
     };
     // operand bytes: chunk 2 kk + h of rows 32 i + l32 (the swizzle has period 16 rows)
     uint32_t offX[2], offW[2];
@@ -147,11 +165,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
 
     // ---- ahead of the main loop: scales, t as MFMA operands (lane: token l32, ranks 8 h .. of
     // each 16) and the first 64 rows of B, 16 bytes along n per lane
-    for (int i = tid; i < kBN; i += kThreads) swt[i] = sw[min(n0 + i, N - 1)];
-    float sxv[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) sxv[i] = sx[min(m0 + 32 * (MT * wm + i) + l32, M - 1)];
-    const rsrc_t trs = buf_rsrc(r ? t + (int64_t)m0 * r : nullptr, (uint64_t)min(M - m0, kBM) * r * 2);
+    const rsrc_t trs = buf_rsrc(LORA ? t + (int64_t)m0 * r : nullptr, (uint64_t)min(M - m0, kBM) * r * 2);
     auto load_t = [&](int i, int kk) __attribute__((always_inline)) {
         const int row = 32 * (MT * wm + i) + l32, j = 16 * kk + 8 * h;
         if (VEC)
@@ -159,7 +173,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
                                                    trs, j < r ? (uint32_t)(row * r + j) * 2u : 0x80000000u, 0, 0));
         return m0 + row < M && j < r ? load8(t + (int64_t)(m0 + row) * r + j, j, r) : u32x4_t{0u, 0u, 0u, 0u};
     };
-    const rsrc_t brs = buf_rsrc(r ? B + n0 : nullptr, r ? ((uint64_t)r * N - n0) * 2 : 0);
+    const rsrc_t brs = buf_rsrc(LORA ? B + n0 : nullptr, LORA ? ((uint64_t)r * N - n0) * 2 : 0);
     constexpr int kCh = kBN / 8, kBPer = 64 * kCh / kThreads;   // 16-byte chunks of a row; per thread of 64 rows
     auto load_b = [&](int j0, int e) __attribute__((always_inline)) {
         const int c = tid + kThreads * e, j = j0 + c / kCh, n = 8 * (c % kCh);
@@ -170,7 +184,14 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
         return j < r && n0 + n < N ? load8(B + (int64_t)j * N + n0 + n, n0 + n, N) : u32x4_t{0u, 0u, 0u, 0u};
     };
     u32x4_t tv[MT][4], bv[kBPer];
-    if (r) {
+    load(s0, 0);
+    load(s1, 1);
+    static_assert(kBN <= kThreads, "a scale per thread");
+    const float swv = sw[min(n0 + tid, N - 1)];
+    float sxv[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sxv[i] = sx[min(m0 + 32 * (MT * wm + i) + l32, M - 1)];
+    if (LORA) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -178,28 +199,29 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
 #pragma unroll
         for (int e = 0; e < kBPer; ++e) bv[e] = load_b(0, e);
     }
-
+    __builtin_amdgcn_sched_barrier(0);
+    load(s2, 2);
+    // zeros from the matrix unit while the first tiles are on their way: writing 256 registers
+    // (and the compiler's copies of them) took a microsecond
     i32x16_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-
-    load(s0, 0);
-    load(s1, 1);
-    load(s2, 2);
-    // tiles 0 and 1 have landed (and the scales are in swt)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
+        for (int j = 0; j < NT; ++j) {
+            const i32x4_t z = {0, 0, 0, 0};
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(z, z, i32x16_t{}, 0, 0, 0);
+        }
+    // tiles 0 and 1 have landed
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
     i32x4_t xa[2][MT], wb[2][NT];
     read(s0, 0, xa[0], wb[0]);
 
     auto step = [&](int ks, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
                     uint8_t* __restrict__ fill) __attribute__((always_inline)) {
-        load(fill, ks + 3);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
+            if (kk == 0) load_x(fill, ks + 3);
+            else load_w(fill, ks + 3);
             if (kk == 0) read(cur, 1, xa[1], wb[1]);
             else read(next, 0, xa[0], wb[0]);
 #pragma unroll
@@ -212,7 +234,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
 #pragma unroll
             for (int g = 0; g < kReads; ++g) {
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                if (kk == 0) __builtin_amdgcn_sched_group_barrier(0x010, (kXL + kWL + kReads - 1) / kReads, 0);
+                if (g % 2 == 1 || kReads < 8) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, kPer > 0 ? kPer : 1, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -229,7 +251,50 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
         step(ks + 3, s3, s0, s2);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last, empty tiles
+    if (tid < kBN) swt[tid] = swv;
     __syncthreads();
+
+    if constexpr (SPLIT) {
+        constexpr uint32_t kTileBytes = (uint32_t)MT * NT * 16 * 4 * kThreads;
+        const int tile = mt * tp.tn + nt;
+        uint64_t* const flags = tp.tags + (size_t)tile * tp.splits;
+        auto off = [&](int i, int j, int v4) { return (uint32_t)((((i * NT + j) * 4 + v4) * kThreads + tid) * 16); };
+        if (split < tp.splits - 1) {
+            const rsrc_t rs = buf_rsrc(tp.part + ((size_t)split * tiles + tile) * kTileBytes, kTileBytes);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4) {
+                        const u32x4_t v = {(uint32_t)acc[i][j][4 * v4], (uint32_t)acc[i][j][4 * v4 + 1],
+                                           (uint32_t)acc[i][j][4 * v4 + 2], (uint32_t)acc[i][j][4 * v4 + 3]};
+                        __builtin_amdgcn_raw_buffer_store_b128(v, rs, off(i, j, v4), 0, kCoherent);
+                    }
+            publish_tag(flags + split, launch_tag());
+            return;
+        }
+        bool fail = wait_tags(flags, tp.splits - 1, launch_tag());
+        if (fail) for (int i = tid; i < kBN; i += kThreads) swt[i] = __builtin_nanf("");
+        for (int p = 0; p < tp.splits - 1; ++p) {
+            const rsrc_t rs = buf_rsrc(tp.part + ((size_t)p * tiles + tile) * kTileBytes, kTileBytes);
+            u32x4_t g[MT][NT][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4)
+                        g[i][j][v4] = __builtin_amdgcn_raw_buffer_load_b128(rs, off(i, j, v4), 0, kCoherent);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] += (int32_t)g[i][j][v >> 2][v & 3];
+        }
+        __syncthreads();
+    }
 
     // ---- epilogue.  B rows go to s1 (0 - 63) and s2 (64 - 127) in their own layout, 16-byte
     // chunks swizzled by row; y leaves through s0 and s3 in turn, 32 tokens of each wave row.
@@ -239,7 +304,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
         const int c = tid + kThreads * e, row = c / kCh, cc = c % kCh;
         *reinterpret_cast<u32x4_t*>(slot + row * kBRow + 16 * (cc ^ ((row & 3) << 1))) = v;
     };
-    if (r) {
+    if (LORA) {
 #pragma unroll
         for (int e = 0; e < kBPer; ++e) put_b(s1, e, bv[e]);
         if (r > 64) {
@@ -251,12 +316,13 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
         __syncthreads();
     }
     const int tj = l32 & 15, tg = l32 >> 4;
+    const rsrc_t yrs = buf_rsrc(y + (int64_t)m0 * N, VEC ? (uint64_t)min(M - m0, kBM) * N * 2 : 0);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         f32x16_t f[NT];
-        // 256 sums live in the accumulation registers until their turn (the compiler would
-        // move all of them to vector registers at the end of the loop, and spill)
-        if constexpr (MT * NT >= 16)
+        // The sums live in the accumulation registers until their turn (the compiler would move
+        // all of them to vector registers at the end of the loop, and spill).
+        if constexpr (MT * NT >= 12)
 #pragma unroll
             for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
@@ -279,10 +345,15 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
                 f[j] = mfma16<DT>(b, a, f[j]);
             }
         };
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            if (16 * kk < r) rank16(s1, kk, tv[i][kk]);
-        for (int kk = 4; 16 * kk < r; ++kk) rank16(s2, kk - 4, load_t(i, kk));
+        if (LORA) {   // (ranks past r are zero: 32 at a time, so that the sums keep their registers)
+            rank16(s1, 0, tv[i][0]);
+            rank16(s1, 1, tv[i][1]);
+            if (r > 32) {
+                rank16(s1, 2, tv[i][2]);
+                rank16(s1, 3, tv[i][3]);
+            }
+            for (int kk = 4; 16 * kk < r; ++kk) rank16(s2, kk - 4, load_t(i, kk));
+        }
         // lane (h, l32): token l32 of the 32, outputs 32 j + 8 v4 + 4 h + 0..3
         if (!VEC) {
             const int m = m0 + 32 * (MT * wm + i) + l32;
@@ -296,7 +367,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
             continue;
         }
         uint8_t* const slot = (i & 1) ? s3 : s0;
-        constexpr int kMask = (kCh < 16 ? kCh : 16) - 1;   // 16-byte chunks of a row are swizzled by the token
+        constexpr int kMask = kCh % 16 == 0 ? 15 : 7;   // 16-byte chunks of a row are swizzled by the token
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -310,48 +381,92 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 16 ? 1 : 2) void int8_gem
 #pragma unroll
         for (int e = 0; e < NWM * 32 * kCh / kThreads; ++e) {
             const int c = tid + kThreads * e, cc = c % kCh, rr = c / kCh;
-            const int m = m0 + 32 * (MT * (rr >> 5) + i) + (rr & 31), n = n0 + 8 * cc;
+            const int row = 32 * (MT * (rr >> 5) + i) + (rr & 31), n = n0 + 8 * cc;
             const u32x4_t v = *reinterpret_cast<const u32x4_t*>(slot + rr * kBRow + 16 * (cc ^ (rr & kMask)));
-            if (m < M && n < N) *reinterpret_cast<u32x4_t*>(y + (int64_t)m * N + n) = v;
+            // rows past M lie past the buffer and are dropped, as are columns past N
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, yrs, n < N ? ((uint32_t)row * (uint32_t)N + (uint32_t)n) * 2u : 0x80000000u, 0, 0);
         }
     }
 }
 
-template <int NWM, int NWN, int MT, int NT>
-qlora_status run(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const uint16_t* t,
-                 const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt, hipStream_t s) {
-    constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN;
-    TileMap tp;
-    tp.tm = (int)(((int64_t)M + kBM - 1) / kBM);
-    tp.tn = (int)(((int64_t)N + kBN - 1) / kBN);
+struct Args {
+    const int8_t* xq;
+    const float* sx;
+    const int8_t* wq;
+    const float* sw;
+    const uint16_t* t;
+    const uint16_t* B;
+    uint16_t* y;
+    int M, N, K, r, dt;
+    hipStream_t s;
+};
+
+template <int NWM, int NWN, int MT, int NT, bool SPLIT>
+qlora_status run(const Args& a, int splits, void* ws) {
+    constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN, kThreads = 64 * NWM * NWN;
+    TileMap tp{};
+    tp.tm = (int)(((int64_t)a.M + kBM - 1) / kBM);
+    tp.tn = (int)(((int64_t)a.N + kBN - 1) / kBN);
     tp.gm = 4;
-    const int64_t total = (int64_t)tp.tm * tp.tn;
-    if (total * 64 * NWM * NWN >= (int64_t(1) << 32) || (int64_t)tp.gm * tp.tn >= (int64_t(1) << 31))
+    const int64_t tiles = (int64_t)tp.tm * tp.tn;
+    if (SPLIT) {
+        const int steps = a.K / kStep;
+        tp.per = (steps + splits - 1) / splits;
+        tp.splits = (steps + tp.per - 1) / tp.per;
+        tp.tags = static_cast<uint64_t*>(ws);
+        tp.part = static_cast<uint8_t*>(ws) + align256((size_t)tiles * splits * 8);
+    }
+    const int64_t total = tiles * (SPLIT ? tp.splits : 1);
+    if (total * kThreads >= (int64_t(1) << 32) || (int64_t)tp.gm * tp.tn >= (int64_t(1) << 31))
         return QLORA_ERR_UNSUPPORTED_SHAPE;
-    // (the offsets of B must fit a buffer's 31 bits)
-    const bool vec = r % 8 == 0 && N % 8 == 0 && (int64_t)r * N * 2 < (int64_t(1) << 31);
-    with_dt(dt, [&](auto dtc) {
+    // (the offsets of B and of a tile's rows of y must fit a buffer's 31 bits)
+    const bool vec = a.r % 8 == 0 && a.N % 8 == 0 && (int64_t)std::max(a.r, kBM) * a.N * 2 < (int64_t(1) << 31);
+    with_dt(a.dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
-        if (vec)
-            hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, true, DT>), dim3((unsigned)total),
-                               dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
-        else
-            hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, false, DT>), dim3((unsigned)total),
-                               dim3(64 * NWM * NWN), 0, s, xq, sx, wq, sw, t, B, y, M, N, K, r, tp);
+#define QL_F(L, V)                                                                                                   \
+    hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, SPLIT, L, V, DT>), dim3((unsigned)total),            \
+                       dim3(kThreads), 0, a.s, a.xq, a.sx, a.wq, a.sw, a.t, a.B, a.y, a.M, a.N, a.K, a.r, tp)
+        if (a.r) {
+            if (vec) QL_F(true, true); else QL_F(true, false);
+        } else {
+            if (vec) QL_F(false, true); else QL_F(false, false);
+        }
+#undef QL_F
     });
     return launch_status();
 }
 
+struct Choice {
+    int tile, splits;   // tile: 0 256x256, 1 256x192, 2 128x128, 3 64x64
+};
+Choice choose(int64_t M, int64_t N, int64_t K) {
+    if (const char* e = getenv("QCFG")) return Choice{e[0] - '0', e[1] ? atoi(e + 1) : 1};
+    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+    const int64_t mid = ((M + 127) / 128) * ((N + 127) / 128);
+    if (big >= 200) return Choice{0, 1};
+    if (mid >= 200 && M > 64) return Choice{2, 1};
+    return Choice{3, 1};
+}
+
 }  // namespace
+
+size_t int8_gemm_fwd_workspace(int64_t M, int64_t N, int64_t K) {
+    const Choice c = choose(M, N, K);
+    if (c.splits <= 1) return 0;
+    const int64_t tiles = c.tile == 2 ? ((M + 127) / 128) * ((N + 127) / 128) : ((M + 63) / 64) * ((N + 63) / 64);
+    return align256((size_t)tiles * c.splits * 8) + (size_t)tiles * (c.splits - 1) * (c.tile == 2 ? 65536 : 16384);
+}
 
 qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                   const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
-                                  hipStream_t s) {
-    const int64_t big = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
-    const int64_t mid = (((int64_t)M + 127) / 128) * (((int64_t)N + 127) / 128);
-    if (big >= 200) return run<2, 2, 4, 4>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
-    if (mid >= 200 && M > 64) return run<2, 2, 2, 2>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
-    return run<2, 2, 1, 1>(xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s);
+                                  void* ws, hipStream_t s) {
+    const Args a{xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s};
+    const Choice c = choose(M, N, K);
+    if (c.tile == 0) return run<2, 2, 4, 4, false>(a, 1, nullptr);
+    if (c.tile == 1) return run<2, 2, 4, 3, false>(a, 1, nullptr);
+    if (c.tile == 2) return c.splits > 1 && ws ? run<2, 2, 2, 2, true>(a, c.splits, ws) : run<2, 2, 2, 2, false>(a, 1, nullptr);
+    return c.splits > 1 && ws ? run<2, 2, 1, 1, true>(a, c.splits, ws) : run<2, 2, 1, 1, false>(a, 1, nullptr);
 }
 
 }  // namespace qlora
