@@ -4,19 +4,21 @@
 //
 // ("bitsandbytes deep dive", section 4: vector-wise int8; sections 8.6 / 12.4: the LoRA
 // branch.)  Both operands are int8 rows with consecutive k, so both tiles are copied
-// HBM -> LDS by direct loads (64 k per step, 16 bytes per lane, XOR-swizzled on the global
-// side) into a ring of four steps, and a lane's MFMA operand is one 16-byte LDS read.
-// Step ks requests tile ks + 3 and reads its own first operands before the barrier that
-// ends step ks - 1; that barrier only waits for the loads of two steps before, so neither
-// the loads nor the LDS latency is exposed.  Sums are exact int32; the scales, t B (r more
-// reduction steps of the 16-bit MFMA on the same accumulators) and the rounding follow
-// once per tile.
+// HBM -> LDS by direct loads (16 bytes per lane, XOR-swizzled on the global side) and a
+// lane's MFMA operand is one 16-byte LDS read.  Operands are read two MFMA depths ahead and
+// tiles are requested one or more steps ahead, so neither latency is exposed: in the main
+// loop of a 256 x 256 tile on an otherwise idle chip a step takes its MFMAs' time (0.44 us
+// per 64 k).  On the whole chip the clock falls to 1.5 - 1.65 GHz, and what a tile moves
+// counts: rows of 128 bytes per step (whole cache lines) measured 6 - 9 % faster than rows
+// of 64 (8192 x 28672 x 8192, r = 0: 1592 to 1475 us; 128 x 128 tiles 12 - 20 %).  Sums are
+// exact int32; the scales, t B (r more reduction steps of the 16-bit MFMA) and the rounding
+// follow once per tile.
 //
 // W rows are the MFMA's first operand, so a lane holds one token m and groups of four
 // consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.  t, the
 // first 64 rows of B and the scales are fetched before the main loop into registers that it
 // has no use for, and the epilogue goes 32 tokens at a time (scale, t B, round, store).
-#include <cstdlib>
+#include <algorithm>
 
 #include "int8.h"
 #include "lora_plan.h"
@@ -68,13 +70,14 @@ __device__ __forceinline__ __attribute__((address_space(3))) T* as_lds(const voi
     return (__attribute__((address_space(3))) T*)(p);
 }
 
-constexpr int kStep = 64;   // reduction per step: bytes of a tile row
-constexpr int kRing = 4;
 
-// Byte of 16-byte chunk c of tile row `row`: 64-byte rows, chunks XOR-swizzled so that any
+// Byte of 16-byte chunk c of tile row `row`: rows of S bytes, chunks XOR-swizzled so that any
 // 16 consecutive rows of one chunk cover all 64 banks.
+template <int S>
+__device__ __forceinline__ int swizzle(int row) { return S == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
+template <int S>
 __device__ __forceinline__ uint32_t tile_byte(int row, int c) {
-    return (uint32_t)row * 64u + ((uint32_t)(c ^ ((row >> 2) & 3)) << 4);
+    return (uint32_t)row * S + ((uint32_t)(c ^ swizzle<S>(row)) << 4);
 }
 
 // Tiles in groups of `gm` row tiles, down the rows first: 32 consecutive tiles (one XCD's
@@ -93,24 +96,29 @@ __device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int
     mt = g * tp.gm + in - nt * rows;
 }
 
-// NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs.  VEC: r % 8 == 0 and
+// NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs; S k per step, RING
+// steps' tiles in LDS.  VEC: r % 8 == 0 and
 // N % 8 == 0, so t, B and y are accessed 16 bytes at a time.
 // LORA: r > 0.  SPLIT: the reduction is split over workgroups; the last part's adds the others' int32 sums
 // (exact, so y does not depend on the split).
-template <int NWM, int NWN, int MT, int NT, bool SPLIT, bool LORA, bool VEC, int DT>
-__global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gemm_fwd_kernel(
+template <int NWM, int NWN, int MT, int NT, int S, int RING, bool SPLIT, bool LORA, bool VEC, int DT>
+__global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void int8_gemm_fwd_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ sx, const int8_t* __restrict__ wq,
     const float* __restrict__ sw, const uint16_t* __restrict__ t, const uint16_t* __restrict__ B,
     uint16_t* __restrict__ y, int M, int N, int K, int r, TileMap tp) {
     constexpr int kWaves = NWM * NWN, kThreads = 64 * kWaves;
     constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN;
-    constexpr int kXB = kBM * kStep, kWB = kBN * kStep;      // bytes of a step's tiles
+    constexpr int kXB = kBM * S, kWB = kBN * S, kKK = S / 32;      // bytes of a step's tiles
     constexpr int kXL = kXB / 1024 / kWaves, kWL = kWB / 1024 / kWaves;   // loads per wave
     static_assert(kXL * kWaves * 1024 == kXB && kWL * kWaves * 1024 == kWB, "tiles are whole wave loads");
     __shared__ __attribute__((aligned(16))) uint8_t s0[kXB + kWB];
     __shared__ __attribute__((aligned(16))) uint8_t s1[kXB + kWB];
-    __shared__ __attribute__((aligned(16))) uint8_t s2[kXB + kWB];
-    __shared__ __attribute__((aligned(16))) uint8_t s3[kXB + kWB];
+    constexpr int kTwo = RING > 2 ? kXB + kWB : 16, kMore = RING > 4 ? kXB + kWB : 16;
+    __shared__ __attribute__((aligned(16))) uint8_t s2[kTwo], s3[kTwo];
+    __shared__ __attribute__((aligned(16))) uint8_t s4[kMore], s5[kMore], s6[kMore], s7[kMore];
+    uint8_t* const slots[8] = {s0, s1, s2, s3, s4, s5, s6, s7};
+    static_assert((RING == 2 && S == 128) || RING == 4 || RING == 8, "slots of the ring");
+    constexpr int kInFlight = RING == 2 ? kXL + kWL : (RING - 3) * (kXL + kWL);   // loads that a barrier leaves in flight
     __shared__ __attribute__((aligned(16))) float swt[kBN];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -119,22 +127,28 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
     int mt, nt;
     tile_of(tp, (int)blockIdx.x - split * tiles, mt, nt);
     const int m0 = mt * kBM, n0 = nt * kBN;
-    const int s_first = SPLIT ? split * tp.per : 0, NS = SPLIT ? min(tp.per, K / kStep - s_first) : K / kStep;
+    const int steps = (K + S - 1) / S, s_first = SPLIT ? split * tp.per : 0, NS = SPLIT ? min(tp.per, steps - s_first) : steps;
 
     // panels as buffers: rows past the end read as zero (the range check covers voffset)
-    const uint32_t k_first = (uint32_t)(s_first * kStep);
+    const uint32_t k_first = (uint32_t)(s_first * S);
     const i32x4_t xrs = buffer_rsrc(xq + (int64_t)m0 * K + k_first, (uint32_t)min(M - m0, kBM) * (uint32_t)K - k_first);
     const i32x4_t wrs = buffer_rsrc(wq + (int64_t)n0 * K + k_first, (uint32_t)min(N - n0, kBN) * (uint32_t)K - k_first);
-    // a wave load fills 16 rows of 64 bytes; lane: row lane / 4, LDS chunk lane % 4
-    const int lrow = lane >> 2, lch = (lane & 3) ^ ((lrow >> 2) & 3);
-    const uint32_t voff = (uint32_t)(16 * wave + lrow) * (uint32_t)K + 16u * (uint32_t)lch;
+    // a wave load fills kRL whole rows of S bytes; lane: row lane / kCL, LDS chunk lane % kCL
+    constexpr int kCL = S / 16, kRL = 64 / kCL;
+    const int lrow = lane / kCL, lch = (lane % kCL) ^ swizzle<S>(kRL * wave + lrow);
+    static_assert(kRL * kWaves % 16 == 0, "the swizzle of a lane's chunk is the same for its next rows");
+    const uint32_t voff = (uint32_t)(kRL * wave + lrow) * (uint32_t)K + 16u * (uint32_t)lch;
+    // of a last step that is wider than what is left of K (64 of 128), the rest reads zero
+    auto past = [&](int ks) __attribute__((always_inline)) {
+        return S == 64 || (int)k_first + ks * S + 16 * lch < K ? 0u : 0x80000000u;
+    };
     auto load_x = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
         i32x4_t rs = xrs;
         rs[2] = ks < NS ? rs[2] : 0;   // steps past K read as zero and move nothing
 #pragma unroll
         for (int j = 0; j < kXL; ++j)
             raw_buffer_load_lds(rs, as_lds<uint32_t>(slot + 1024 * (kWaves * j + wave)), 16,
-                                (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+                                (int)((voff + (uint32_t)(kRL * kWaves * j) * (uint32_t)K) | past(ks)), ks * S, 0, 0);
     };
     auto load_w = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
         i32x4_t rs = wrs;
@@ -142,25 +156,25 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
 #pragma unroll
         for (int j = 0; j < kWL; ++j)
             raw_buffer_load_lds(rs, as_lds<uint32_t>(slot + kXB + 1024 * (kWaves * j + wave)), 16,
-                                (int)(voff + (uint32_t)(16 * kWaves * j) * (uint32_t)K), ks * kStep, 0, 0);
+                                (int)((voff + (uint32_t)(kRL * kWaves * j) * (uint32_t)K) | past(ks)), ks * S, 0, 0);
     };
     auto load = [&](uint8_t* __restrict__ slot, int ks) __attribute__((always_inline)) {
         load_x(slot, ks);
         load_w(slot, ks);
     };
     // operand bytes: chunk 2 kk + h of rows 32 i + l32 (the swizzle has period 16 rows)
-    uint32_t offX[2], offW[2];
+    uint32_t offX[kKK], offW[kKK];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        offX[kk] = tile_byte(32 * MT * wm + l32, 2 * kk + h);
-        offW[kk] = kXB + tile_byte(32 * NT * wn + l32, 2 * kk + h);
+    for (int kk = 0; kk < kKK; ++kk) {
+        offX[kk] = tile_byte<S>(32 * MT * wm + l32, 2 * kk + h);
+        offW[kk] = kXB + tile_byte<S>(32 * NT * wn + l32, 2 * kk + h);
     }
     auto read = [&](const uint8_t* __restrict__ slot, int kk, i32x4_t (&a)[MT], i32x4_t (&b)[NT])
                     __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) b[i] = *reinterpret_cast<const i32x4_t*>(slot + offW[kk] + 2048u * i);
+        for (int i = 0; i < NT; ++i) b[i] = *reinterpret_cast<const i32x4_t*>(slot + offW[kk] + 32u * S * i);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const i32x4_t*>(slot + offX[kk] + 2048u * i);
+        for (int i = 0; i < MT; ++i) a[i] = *reinterpret_cast<const i32x4_t*>(slot + offX[kk] + 32u * S * i);
     };
 
     // ---- ahead of the main loop: scales, t as MFMA operands (lane: token l32, ranks 8 h .. of
@@ -185,7 +199,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
     };
     u32x4_t tv[MT][4], bv[kBPer];
     load(s0, 0);
-    load(s1, 1);
+    if (RING > 2) load(s1, 1);
     static_assert(kBN <= kThreads, "a scale per thread");
     const float swv = sw[min(n0 + tid, N - 1)];
     float sxv[MT];
@@ -200,7 +214,9 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
         for (int e = 0; e < kBPer; ++e) bv[e] = load_b(0, e);
     }
     __builtin_amdgcn_sched_barrier(0);
-    load(s2, 2);
+    if (RING == 2) load(s1, 1);
+#pragma unroll
+    for (int p = 2; p < RING - 1; ++p) load(slots[p], p);
     // zeros from the matrix unit while the first tiles are on their way: writing 256 registers
     // (and the compiler's copies of them) took a microsecond
     i32x16_t acc[MT][NT];
@@ -211,25 +227,31 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
             const i32x4_t z = {0, 0, 0, 0};
             acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(z, z, i32x16_t{}, 0, 0, 0);
         }
-    // tiles 0 and 1 have landed
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
+    // tiles 0 and 1 (of two slots, 0) have landed
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
     i32x4_t xa[2][MT], wb[2][NT];
     read(s0, 0, xa[0], wb[0]);
+    read(s0, 1, xa[1], wb[1]);
 
-    auto step = [&](int ks, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
-                    uint8_t* __restrict__ fill) __attribute__((always_inline)) {
+    auto step = [&](int ks, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next, uint8_t* __restrict__ fill) __attribute__((always_inline)) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (kk == 0) load_x(fill, ks + 3);
-            else load_w(fill, ks + 3);
-            if (kk == 0) read(cur, 1, xa[1], wb[1]);
-            else read(next, 0, xa[0], wb[0]);
+        for (int kk = 0; kk < kKK; ++kk) {
+            if (kk == 0) load_x(fill, ks + RING - 1);
+            if (kk == kKK / 2) load_w(fill, ks + RING - 1);
+            // operands two MFMA depths ahead: an LDS read's latency is longer than a small tile's MFMAs
+            i32x4_t xn[MT], wn_[NT];
+            if (kk + 2 < kKK) read(cur, kk + 2, xn, wn_);
+            else read(next, kk + 2 - kKK, xn, wn_);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wb[kk][j], xa[kk][i], acc[i][j], 0, 0, 0);
-            // the next half's operands are read (and the new tiles requested) between the MFMAs
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wb[kk & 1][j], xa[kk & 1][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xa[kk & 1][i] = xn[i];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wb[kk & 1][j] = wn_[j];
+            // operands are read (and the new tiles requested) between the MFMAs
             constexpr int kReads = MT + NT, kPer = MT * NT / kReads;
 #pragma unroll
             for (int g = 0; g < kReads; ++g) {
@@ -239,16 +261,54 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        // tile ks + 2 has landed once only this step's own loads are in flight
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kXL + kWL) : "memory");
+        // tile ks + 2 has landed once only the loads of the RING - 3 after it are in flight
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
+    // Two slots of 128 k (256 x 256: rows of whole 128-byte lines, and no room for a third).  A
+    // tile is in registers after half of its step; the one barrier of a step is there: its tile
+    // may then be overwritten, and the next one, requested a whole step before, has landed.
+    auto step2 = [&](int ks, uint8_t* cur, const uint8_t* next) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < kKK; ++kk) {
+            if (kk == 2) load_x(cur, ks + 2);
+            if (kk == 3) load_w(cur, ks + 2);
+            i32x4_t xn[MT], wn_[NT];
+            if (kk < 2) read(cur, (kk + 2) % kKK, xn, wn_);
+            else read(next, kk - 2, xn, wn_);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wb[kk & 1][j], xa[kk & 1][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xa[kk & 1][i] = xn[i];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wb[kk & 1][j] = wn_[j];
+            constexpr int kReads = MT + NT, kPer = MT * NT / kReads;
+#pragma unroll
+            for (int g = 0; g < kReads; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                if (kk >= 2) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                if (kk == 1) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // reads done by the barrier
+                else __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (kk == 1) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
     // whole turns of the ring: steps past K multiply zeros
-    for (int ks = 0; ks < NS; ks += kRing) {
-        step(ks, s0, s1, s3);
-        step(ks + 1, s1, s2, s0);
-        step(ks + 2, s2, s3, s1);
-        step(ks + 3, s3, s0, s2);
+    if constexpr (RING == 2) {
+        for (int ks = 0; ks < NS; ks += 2) {
+            step2(ks, s0, s1);
+            step2(ks + 1, s1, s0);
+        }
+    } else for (int ks = 0; ks < NS; ks += RING) {
+#pragma unroll
+        for (int p = 0; p < RING; ++p) step(ks + p, slots[p], slots[(p + 1) % RING], slots[(p + RING - 1) % RING]);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last, empty tiles
     if (tid < kBN) swt[tid] = swv;
@@ -296,22 +356,27 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
         __syncthreads();
     }
 
-    // ---- epilogue.  B rows go to s1 (0 - 63) and s2 (64 - 127) in their own layout, 16-byte
-    // chunks swizzled by row; y leaves through s0 and s3 in turn, 32 tokens of each wave row.
-    constexpr int kBRow = 2 * kBN;
-    static_assert(64 * kBRow <= kXB + kWB && NWM * 32 * kBRow <= kXB + kWB, "epilogue tiles fit the ring slots");
+    // ---- epilogue, in four parts of the ring.  B rows go to e1 (0 - 63) and e2 (64 - 127) in
+    // their own layout, 16-byte chunks swizzled by row; y leaves through e0 and e3 in turn, 32
+    // tokens of each wave row.
+    constexpr int kBRow = 2 * kBN, kPart = RING == 2 ? (kXB + kWB) / 2 : kXB + kWB;
+    static_assert(64 * kBRow <= kPart && NWM * 32 * kBRow <= kPart, "epilogue tiles fit their parts");
+    uint8_t* const e0 = s0;
+    uint8_t* const e1 = RING == 2 ? s0 + kPart : s1;
+    uint8_t* const e2 = RING == 2 ? s1 : s2;
+    uint8_t* const e3 = RING == 2 ? s1 + kPart : s3;
     auto put_b = [&](uint8_t* slot, int e, u32x4_t v) __attribute__((always_inline)) {
         const int c = tid + kThreads * e, row = c / kCh, cc = c % kCh;
         *reinterpret_cast<u32x4_t*>(slot + row * kBRow + 16 * (cc ^ ((row & 3) << 1))) = v;
     };
     if (LORA) {
 #pragma unroll
-        for (int e = 0; e < kBPer; ++e) put_b(s1, e, bv[e]);
+        for (int e = 0; e < kBPer; ++e) put_b(e1, e, bv[e]);
         if (r > 64) {
 #pragma unroll
             for (int e = 0; e < kBPer; ++e) bv[e] = load_b(64, e);
 #pragma unroll
-            for (int e = 0; e < kBPer; ++e) put_b(s2, e, bv[e]);
+            for (int e = 0; e < kBPer; ++e) put_b(e2, e, bv[e]);
         }
         __syncthreads();
     }
@@ -346,13 +411,13 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
             }
         };
         if (LORA) {   // (ranks past r are zero: 32 at a time, so that the sums keep their registers)
-            rank16(s1, 0, tv[i][0]);
-            rank16(s1, 1, tv[i][1]);
+            rank16(e1, 0, tv[i][0]);
+            rank16(e1, 1, tv[i][1]);
             if (r > 32) {
-                rank16(s1, 2, tv[i][2]);
-                rank16(s1, 3, tv[i][3]);
+                rank16(e1, 2, tv[i][2]);
+                rank16(e1, 3, tv[i][3]);
             }
-            for (int kk = 4; 16 * kk < r; ++kk) rank16(s2, kk - 4, load_t(i, kk));
+            for (int kk = 4; 16 * kk < r; ++kk) rank16(e2, kk - 4, load_t(i, kk));
         }
         // lane (h, l32): token l32 of the 32, outputs 32 j + 8 v4 + 4 h + 0..3
         if (!VEC) {
@@ -366,7 +431,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 12 ? 1 : 2) void int8_gem
                 }
             continue;
         }
-        uint8_t* const slot = (i & 1) ? s3 : s0;
+        uint8_t* const slot = (i & 1) ? e3 : e0;
         constexpr int kMask = kCh % 16 == 0 ? 15 : 7;   // 16-byte chunks of a row are swizzled by the token
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -402,7 +467,7 @@ struct Args {
     hipStream_t s;
 };
 
-template <int NWM, int NWN, int MT, int NT, bool SPLIT>
+template <int NWM, int NWN, int MT, int NT, int S, int RING, bool SPLIT>
 qlora_status run(const Args& a, int splits, void* ws) {
     constexpr int kBM = 32 * MT * NWM, kBN = 32 * NT * NWN, kThreads = 64 * NWM * NWN;
     TileMap tp{};
@@ -411,7 +476,7 @@ qlora_status run(const Args& a, int splits, void* ws) {
     tp.gm = 4;
     const int64_t tiles = (int64_t)tp.tm * tp.tn;
     if (SPLIT) {
-        const int steps = a.K / kStep;
+        const int steps = (a.K + S - 1) / S;
         tp.per = (steps + splits - 1) / splits;
         tp.splits = (steps + tp.per - 1) / tp.per;
         tp.tags = static_cast<uint64_t*>(ws);
@@ -425,7 +490,7 @@ qlora_status run(const Args& a, int splits, void* ws) {
     with_dt(a.dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
 #define QL_F(L, V)                                                                                                   \
-    hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, SPLIT, L, V, DT>), dim3((unsigned)total),            \
+    hipLaunchKernelGGL((int8_gemm_fwd_kernel<NWM, NWN, MT, NT, S, RING, SPLIT, L, V, DT>), dim3((unsigned)total),            \
                        dim3(kThreads), 0, a.s, a.xq, a.sx, a.wq, a.sw, a.t, a.B, a.y, a.M, a.N, a.K, a.r, tp)
         if (a.r) {
             if (vec) QL_F(true, true); else QL_F(true, false);
@@ -437,36 +502,76 @@ qlora_status run(const Args& a, int splits, void* ws) {
     return launch_status();
 }
 
+enum { k256x256, k256x192, k128x128, k64x64 };
 struct Choice {
-    int tile, splits;   // tile: 0 256x256, 1 256x192, 2 128x128, 3 64x64
+    int tile, splits;
 };
-Choice choose(int64_t M, int64_t N, int64_t K) {
-    if (const char* e = getenv("QCFG")) return Choice{e[0] - '0', e[1] ? atoi(e + 1) : 1};
-    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-    const int64_t mid = ((M + 127) / 128) * ((N + 127) / 128);
-    if (big >= 200) return Choice{0, 1};
-    if (mid >= 200 && M > 64) return Choice{2, 1};
-    return Choice{3, 1};
+
+inline int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
+// The tile, and the split of the reduction, with the least estimated time in microseconds.
+// A round of n tiles on the 256 CUs takes a start and end plus, per 64 k, the larger of a
+// tile's MFMA time and its share of what the chip sustains; fitted to measurements of the
+// products below (K = 4096 unless given, quantization of x included):
+//   M x N           256x256  256x192  128x128  128x128 split 2  64x64
+//   4096 x 4096        67.8     88.0     84.6           99.2      138
+//   2048 x 11008      101.9     92.1    111.7                     179
+//   1024 x 4096        48.0     41.6     26.8           30.4
+//   512 x 4096                           21.1           21.1     25.1
+//   333 x 4096, K = 11008                40.5           31.0     53.9
+//   100 x 11008                          19.7           19.2     20.9
+//   128 x 4096                           17.0                    13.2
+//   33 x 4096                            17.1           16.5     11.3
+Choice choose(int64_t M, int64_t N, int64_t K, bool may_split) {
+    const double steps = (double)K / 64;
+    auto rounds = [&](int64_t n, double ends, double tile_us, double chip_us) {
+        const double last = (double)(n % 256);
+        return (double)(n / 256) * (ends + steps * chip_us) +
+               (last > 0 ? ends + 4.0 + steps * std::max(tile_us, chip_us * last / 256) : 0.0);
+    };
+    Choice best{k256x256, 1};
+    double us = rounds(tiles_of(M, N, 256, 256), 9.5, 0.44, 0.80);
+    auto offer = [&](double t, int tile, int splits) {
+        if (t < us) {
+            us = t;
+            best = Choice{tile, splits};
+        }
+    };
+    offer(rounds(tiles_of(M, N, 256, 192), 8.0, 0.34, 0.62), k256x192, 1);
+    const int64_t n128 = tiles_of(M, N, 128, 128), n64 = tiles_of(M, N, 64, 64);
+    auto small = [&](int64_t n, double s) {   // 128 x 128, s steps each
+        const double last = (double)(n % 256);
+        return (double)(n / 256) * (2.5 + s * 0.28) + (last > 0 ? 4.0 + s * (0.12 + 0.16 * last / 256) : 0.0);
+    };
+    offer(small(n128, steps), k128x128, 1);
+    // a split adds a partial tile of 64 KB, written and read, and the wait for it
+    if (may_split && K >= 1024)
+        for (int s = 2; s <= 4 && n128 * s <= 256; ++s) offer(small(n128 * s, steps / s) + 3.0 + s, k128x128, s);
+    offer((double)((n64 + 511) / 512) * 3.0 + steps * (0.04 + 0.0005 * (double)n64), k64x64, 1);
+    return best;
 }
 
 }  // namespace
 
 size_t int8_gemm_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-    const Choice c = choose(M, N, K);
-    if (c.splits <= 1) return 0;
-    const int64_t tiles = c.tile == 2 ? ((M + 127) / 128) * ((N + 127) / 128) : ((M + 63) / 64) * ((N + 63) / 64);
-    return align256((size_t)tiles * c.splits * 8) + (size_t)tiles * (c.splits - 1) * (c.tile == 2 ? 65536 : 16384);
+    const Choice c = choose(M, N, K, true);
+    if (c.splits == 1) return 0;
+    const int64_t tiles = tiles_of(M, N, 128, 128);
+    return align256((size_t)(tiles * c.splits) * 8) + (size_t)(tiles * (c.splits - 1)) * 128 * 128 * 4;
 }
 
 qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                   const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
                                   void* ws, hipStream_t s) {
     const Args a{xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s};
-    const Choice c = choose(M, N, K);
-    if (c.tile == 0) return run<2, 2, 4, 4, false>(a, 1, nullptr);
-    if (c.tile == 1) return run<2, 2, 4, 3, false>(a, 1, nullptr);
-    if (c.tile == 2) return c.splits > 1 && ws ? run<2, 2, 2, 2, true>(a, c.splits, ws) : run<2, 2, 2, 2, false>(a, 1, nullptr);
-    return c.splits > 1 && ws ? run<2, 2, 1, 1, true>(a, c.splits, ws) : run<2, 2, 1, 1, false>(a, 1, nullptr);
+    const Choice c = choose(M, N, K, ws != nullptr);
+    switch (c.tile) {
+        case k256x256: return run<2, 2, 4, 4, 128, 2, false>(a, 1, nullptr);
+        case k256x192: return run<2, 2, 4, 3, 128, 2, false>(a, 1, nullptr);
+        case k128x128:
+            return c.splits > 1 ? run<2, 2, 2, 2, 128, 4, true>(a, c.splits, ws) : run<2, 2, 2, 2, 128, 4, false>(a, 1, nullptr);
+        default: return run<2, 2, 1, 1, 64, 8, false>(a, 1, nullptr);
+    }
 }
 
 }  // namespace qlora
