@@ -34,7 +34,7 @@ inline bool bad_sizes(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 struct FwdWs {
-    size_t codes, scale, tbuf, part, gemm, total;  // x in 8 bits; t when the caller keeps none; split sums of t, of y
+    size_t codes, scale, tbuf, part, total;  // x in 8 bits; t when the caller keeps none; the products' own
 };
 inline FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     FwdWs w{};
@@ -48,8 +48,7 @@ inline FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     w.scale = align256((size_t)M * K);
     w.tbuf = w.scale + align256((size_t)M * 4);
     w.part = w.tbuf + align256((size_t)M * r * 2);
-    w.gemm = w.part + (r ? align256(nt_ws_bytes(M, K, r)) : 0);
-    w.total = w.gemm + int8_gemm_fwd_workspace(M, N, K);
+    w.total = w.part + int8_gemm_fwd_workspace(M, N, K);
     return w;
 }
 
@@ -105,16 +104,18 @@ qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64
     int8_t* xq = x_keep ? x_keep->codes : reinterpret_cast<int8_t*>(at(ws, W.codes));
     float* sx = x_keep ? x_keep->scale : reinterpret_cast<float*>(at(ws, W.scale));
     uint16_t* t = t_out ? t_out : reinterpret_cast<uint16_t*>(at(ws, W.tbuf));
-    const bool decode = int8_gemv_supported(M, N, K, r);
-    if (decode && !x_keep && int8_gemv_quantizes(M, K)) xq = nullptr;
-    else if ((st = launch_int8_quantize(x, M, K, xq, sx, dt, s)) != QLORA_OK) return st;
-    if (decode)
-        return launch_int8_gemv(x, xq, sx, w->codes, w->scale, nullptr, A, B, r ? alpha / (float)r : 0.0f, y, t_out,
-                                at(ws, W.part), (int)M, (int)N, (int)K, r, dt, s);
-    if (r && (st = launch_nt(x, A, true, at(ws, W.part), t, alpha / (float)r, (int)M, (int)K, r, dt, s)) != QLORA_OK)
-        return st;
+    const float scale = r ? alpha / (float)r : 0.0f;
+    if (int8_gemv_supported(M, N, K, r)) {
+        if (!x_keep && int8_gemv_quantizes(M, K)) xq = nullptr;
+        else if ((st = launch_int8_quantize(x, M, K, xq, sx, dt, s)) != QLORA_OK) return st;
+        return launch_int8_gemv(x, xq, sx, w->codes, w->scale, nullptr, A, B, scale, y, t_out, at(ws, W.part), (int)M,
+                                (int)N, (int)K, r, dt, s);
+    }
+    st = r ? launch_int8_prep(x, A, scale, (int)M, (int)K, r, xq, sx, t, dt, s)
+           : launch_int8_quantize(x, M, K, xq, sx, dt, s);
+    if (st != QLORA_OK) return st;
     return launch_int8_gemm_fwd(xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, dt,
-                                at(ws, W.gemm), s);
+                                at(ws, W.part), s);
 }
 
 qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const uint16_t* t, const uint16_t* B,
