@@ -112,9 +112,11 @@ size_t int8_gemv_workspace(int r);
 qlora_status launch_int8_gemv(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                               const uint16_t* t, const uint16_t* A, const uint16_t* B, float scale, uint16_t* y,
                               uint16_t* t_out, void* ws, int M, int N, int K, int r, int dt, hipStream_t s);
-// dx = RNE_16(dy W_16 + u A^T); r == 0: no u A^T
+// dx = RNE_16(dy W_16 + u A^T); r == 0: no u A^T.  ws (nullable): int8_gemm_dx_workspace bytes
+// that need no clearing, with which small products split their reduction.
+size_t int8_gemm_dx_workspace(int64_t M, int64_t N, int64_t K);
 qlora_status launch_int8_gemm_bwd_dx(const uint16_t* dy, const int8_t* wq, const float* sw, const uint16_t* u,
-                                     const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt,
+                                     const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt, void* ws,
                                      hipStream_t s);
 
 // LoRA gradients from 8-bit checkpoints: up to kInt8GradLayers layers (two contractions each)

@@ -134,9 +134,12 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
                                 (int)w->cols, r, dt_of(w->dtype), nullptr, (hipStream_t)stream);
 }
 
+// the split sums of u, in front of the product's own
+static size_t dx_product_ws(int64_t M, int64_t N, int r) { return r ? align256(nt_ws_bytes(M, N, r)) : 0; }
+
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r) {
-    if (bad_sizes(M, N, K, r) || M == 0 || r == 0) return 0;
-    return align256(nt_ws_bytes(M, N, r));
+    if (bad_sizes(M, N, K, r) || M == 0 || K % kBlock) return 0;
+    return dx_product_ws(M, N, r) + int8_gemm_dx_workspace(M, N, K);
 }
 
 qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
@@ -156,7 +159,8 @@ qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint
     hipStream_t s = (hipStream_t)stream;
     const int dt = dt_of(w->dtype);
     if (r && (st = launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt, s)) != QLORA_OK) return st;
-    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt, s);
+    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt,
+                                   need ? at(ws, dx_product_ws(M, N, r)) : nullptr, s);
 }
 
 qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
@@ -168,7 +172,7 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
     if (!dy || !dx || (r && (!u || !A)) || (!r && (u || A))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(dx) || !aligned16(u) || !aligned16(A)) return QLORA_ERR_MISALIGNED;
     return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)w->rows, (int)w->cols, r,
-                                   dt_of(w->dtype), (hipStream_t)stream);
+                                   dt_of(w->dtype), nullptr, (hipStream_t)stream);
 }
 
 // Tiles of one launch of the gradient kernel: the layers [i0, i0 + n) of a batch.

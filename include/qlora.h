@@ -429,8 +429,9 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
  * values of the weight as everywhere in this library:
  *   u  = s * (dy B^T)            [M, r]  into the caller's u (kept for the gradients)
  *   dx = dy W_16 + u A^T         [M, K],  W_16[n, k] = RNE_16( fl32( sw[n] * wq[n, k] ) )
- * r == 0: dx = dy W_16 (A, B, u NULL, no workspace).  qlora_int8_gemm_bwd_dx is
- * the dx stage for a given u.  M == 0 is a no-op.  Errors as qlora_linear_bwd_dx. */
+ * r == 0: dx = dy W_16 (A, B, u NULL).  qlora_int8_gemm_bwd_dx is the dx stage for a
+ * given u, with no workspace; it may add dx's fp32 sums in another order than the call
+ * above, which splits long reductions of few tokens: dx may differ in the last bit.  M == 0 is a no-op.  Errors as qlora_linear_bwd_dx. */
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
 qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
                                       float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,

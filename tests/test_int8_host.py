@@ -95,7 +95,7 @@ def test_bwd_dx_arguments(q):
     f, g = q.lib.qlora_int8_linear_bwd_dx, q.lib.qlora_int8_gemm_bwd_dx
     w = _st(q)
     need = int(q.lib.qlora_int8_linear_bwd_dx_workspace(4, 64, 128, 8))
-    assert need > 0 and int(q.lib.qlora_int8_linear_bwd_dx_workspace(4, 64, 128, 0)) == 0
+    assert need > 0 and int(q.lib.qlora_int8_linear_bwd_dx_workspace(4, 64, 128, 0)) < need
 
     def layer(M=4, A=FAKE, B=FAKE, r=8, alpha=1.0, dy=FAKE, u=FAKE, dx=FAKE, ws=FAKE, n=need):
         return f(ctypes.byref(w), M, A, B, r, alpha, dy, u, dx, ws, n, None)
