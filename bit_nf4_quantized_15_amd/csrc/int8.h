@@ -93,6 +93,10 @@ qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols,
 // launch_int8_quantize and t = RNE_16(s x A) [M, r] (1 <= r <= 128) in one launch
 qlora_status launch_int8_prep(const uint16_t* x, const uint16_t* A, float s, int M, int K, int r, int8_t* codes,
                               float* scale, uint16_t* t, int dt, hipStream_t st);
+// u = RNE_16(s dy B^T) [M, r] without split sums, for sizes where that is faster
+bool int8_u_supported(int64_t M, int64_t N, int r);
+qlora_status launch_int8_u(const uint16_t* dy, const uint16_t* B, float s, int M, int N, int r, uint16_t* u, int dt,
+                           hipStream_t st);
 qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int dt,
                                     uint16_t* out, hipStream_t s);
 // y = RNE_16(sx sw (xq wq^T) + t B); r == 0: no t B.  ws (nullable): int8_gemm_fwd_workspace

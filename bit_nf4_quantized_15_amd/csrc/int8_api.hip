@@ -158,7 +158,11 @@ qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
     const int dt = dt_of(w->dtype);
-    if (r && (st = launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt, s)) != QLORA_OK) return st;
+    if (r) {
+        st = int8_u_supported(M, N, r) ? launch_int8_u(dy, B, alpha / (float)r, (int)M, (int)N, r, u, dt, s)
+                                       : launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt, s);
+        if (st != QLORA_OK) return st;
+    }
     return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt,
                                    need ? at(ws, dx_product_ws(M, N, r)) : nullptr, s);
 }

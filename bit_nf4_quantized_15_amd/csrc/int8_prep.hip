@@ -206,7 +206,97 @@ __global__ __launch_bounds__(kThreads, 2) void int8_prep_kernel(const uint16_t* 
     }
 }
 
+// The same for the backward's u = RNE_16(s dy B^T) [M, r]: B [r, N] has consecutive n in its
+// rows, so its operands come straight from memory, and there are no codes.  N % 8 == 0.
+template <int TQ, int DT>
+__global__ __launch_bounds__(kThreads, 2) void int8_u_kernel(const uint16_t* __restrict__ dy,
+                                                             const uint16_t* __restrict__ B, float s, int M, int N,
+                                                             int r, uint16_t* __restrict__ u) {
+    __shared__ __attribute__((aligned(16))) f32x4_t red[kWaves * TQ * 64];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const int rows = (int)min((int64_t)16, M - m0), steps = (N + 63) >> 6;
+    const rsrc_t drs = buf_rsrc(dy + m0 * N, (uint64_t)rows * N * 2);
+    const rsrc_t brs = buf_rsrc(B, (uint64_t)r * N * 2);
+    struct Step {
+        u32x4_t x[2], b[TQ][2];
+    };
+    auto load = [&](Step& q, int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int n = 64 * st + 16 * g + 8 * c;
+            const bool on = n < N;                          // (columns past N would be the next row's)
+            q.x[c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                drs, on ? ((uint32_t)i * (uint32_t)N + (uint32_t)n) * 2u : kNone, 0, 0));
+#pragma unroll
+            for (int t = 0; t < TQ; ++t)                    // (rows past r lie past the buffer)
+                q.b[t][c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                    brs, on ? ((uint32_t)(16 * t + i) * (uint32_t)N + (uint32_t)n) * 2u : kNone, 0, 0));
+        }
+    };
+    f32x4_t acc[TQ];
+#pragma unroll
+    for (int t = 0; t < TQ; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int P = TQ <= 4 ? 4 : 2;                      // steps in flight
+    Step ring[P];
+#pragma unroll
+    for (int p = 0; p < P - 1; ++p) load(ring[p], wave + kWaves * p);
+    for (int st = wave; st < steps; st += P * kWaves) {     // steps past N multiply zeros
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            load(ring[(p + P - 1) % P], st + kWaves * (p + P - 1));
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int t = 0; t < TQ; ++t) acc[t] = mfma16<DT>(ring[p].b[t][c], ring[p].x[c], acc[t]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TQ; ++t) red[(wave * TQ + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    for (int v = tid; v < TQ * 64; v += kThreads) {
+        const int l = v & 63, t = v >> 6, m = l & 15;
+        f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const f32x4_t z = red[(w * TQ + t) * 64 + l];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += z[e];
+        }
+        if (m < rows)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 16 * t + 4 * (l >> 4) + e;
+                if (j < r) u[(m0 + m) * r + j] = (uint16_t)(pack2<DT>(s * sum[e], 0.0f) & 0xFFFFu);
+            }
+    }
+}
+
 }  // namespace
+
+// Up to 1024 tokens and 5120 columns: 300 x 4096, r = 16 (the whole dx call) 46.0 us with
+// split sums and 40.2 here, 512 x 4096, r = 64 65.3 and 58.3; 2048 x 4096 83.2 and 90.7, 1024 x
+// 11008 118.4 and 148.5 (every workgroup reads all of B).
+bool int8_u_supported(int64_t M, int64_t N, int r) { return N % 8 == 0 && N <= 5120 && M <= 1024 && r <= 128; }
+
+qlora_status launch_int8_u(const uint16_t* dy, const uint16_t* B, float s, int M, int N, int r, uint16_t* u, int dt,
+                           hipStream_t st) {
+    const int64_t grid = ((int64_t)M + 15) / 16;
+    if (grid * kThreads >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    with_dt(dt, [&](auto dtc) {
+        constexpr int DT = decltype(dtc)::value;
+#define QL_U(TQ) \
+    hipLaunchKernelGGL((int8_u_kernel<TQ, DT>), dim3((unsigned)grid), dim3(kThreads), 0, st, dy, B, s, M, N, r, u)
+        if (r <= 16) QL_U(1);
+        else if (r <= 32) QL_U(2);
+        else if (r <= 64) QL_U(4);
+        else QL_U(8);
+#undef QL_U
+    });
+    return launch_status();
+}
 
 qlora_status launch_int8_prep(const uint16_t* x, const uint16_t* A, float s, int M, int K, int r, int8_t* codes,
                               float* scale, uint16_t* t, int dt, hipStream_t st) {
