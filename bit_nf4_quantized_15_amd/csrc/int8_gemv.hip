@@ -42,8 +42,6 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
 }
 
 constexpr int kWaves = 8, kThreads = 512, kRows = 16;
-constexpr int kTLd = 136;                 // halves of a row of t and of B's 16 columns in LDS (ranks up to 128)
-constexpr int kTBytes = kRows * kTLd * 2;
 constexpr int kProducers = 8;
 constexpr uint32_t kSelfBytes = 72u << 10;
 
@@ -64,9 +62,13 @@ struct GemvArgs {
     float scale;
 };
 
-// LDS: two reduction buffers, two B tiles, t, 16 scales and the wait's verdict, then x's codes.
-constexpr int kRedBytes = kWaves * 64 * 16;
-constexpr int kOffB = 2 * kRedBytes, kOffT = kOffB + 2 * kTBytes, kOffS = kOffT + kTBytes, kOffX = kOffS + 256;
+// LDS: 16 scales and the wait's verdict, a reduction buffer, B's 16 columns and t (rows of
+// their rank, in whole 32s, and 8 halves), then x's codes.  16 tokens of 4096 at rank 64 leave
+// room for two workgroups on a CU.
+constexpr int kOffS = 0, kOffRed = 256, kOffB = kOffRed + kWaves * 64 * 16;
+__host__ __device__ constexpr int t_ld(int r) { return ((r + 31) & ~31) + 8; }
+__host__ __device__ constexpr int off_t(int r) { return kOffB + (r ? kRows * t_ld(r) * 2 : 0); }
+__host__ __device__ constexpr int off_x(int r) { return off_t(r) + (r ? kRows * t_ld(r) * 2 : 0); }
 
 // Partial products of x A over this producer's range of K: [16][rp] fp32.
 template <int DT>
@@ -137,7 +139,7 @@ struct SelfQuant {
         }
     }
     __device__ __forceinline__ void run(const GemvArgs& a, int wave, int lane, uint8_t* lds) {
-        uint32_t* const am = reinterpret_cast<uint32_t*>(lds);      // [wave]
+        uint32_t* const am = reinterpret_cast<uint32_t*>(lds + kOffRed);   // [wave]
         float* const sxs = reinterpret_cast<float*>(lds + kOffS);
         const int per = kWaves / G, part = wave % G;
         for (int p = 0; p * per < a.M; ++p) {
@@ -167,7 +169,7 @@ struct SelfQuant {
             __syncthreads();
             for (int e = 0; e < G; ++e) top = max(top, am[wave - part + e]);
             const RowScale rs = row_scale<DT>(top);
-            uint8_t* const xl = lds + kOffX + (size_t)min(row, a.M - 1) * (a.K + 16);
+            uint8_t* const xl = lds + off_x(a.r) + (size_t)min(row, a.M - 1) * (a.K + 16);
             if (on) {
                 if (part == 0 && lane == 0) sxs[row] = rs.scale;
 #pragma unroll
@@ -231,13 +233,15 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
 
     const int rp32 = (a.r + 31) & ~31;
     const rsrc_t brs = buf_rsrc(a.r ? a.B : nullptr, (uint32_t)a.r * (uint32_t)a.N * 2u);
-    uint16_t* const tl = reinterpret_cast<uint16_t*>(lds + kOffT);
+    const int ld = t_ld(a.r), xat = off_x(a.r);
+    uint16_t* const tl = reinterpret_cast<uint16_t*>(lds + off_t(a.r));
+    uint16_t* const bt = reinterpret_cast<uint16_t*>(lds + kOffB);
+    uint8_t* const red = lds + kOffRed;
     i32x4_t acc = {0, 0, 0, 0};
     int turn = 0;                                       // row tiles done
     auto finish = [&]() __attribute__((always_inline)) {
         const int n0 = tile * kRows;
-        uint8_t* const red = lds + (turn & 1) * kRedBytes;
-        uint16_t* const bt = reinterpret_cast<uint16_t*>(lds + kOffB + (turn & 1) * kTBytes);
+        if (turn) __syncthreads();   // (the buffers of the tile before have been read)
         *reinterpret_cast<i32x4_t*>(red + (wave * 64 + lane) * 16) = acc;
         // B's 16 columns, [n][j]: zero past r
         uint16_t bv[4];
@@ -277,14 +281,14 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
                     }
                     if (a.t_out && (int)blockIdx.x == a.P) a.t_out[(int64_t)m * a.r + j] = o;
                 }
-                tl[m * kTLd + j] = o;
+                tl[m * ld + j] = o;
             }
         }
         if (a.r)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (32 * e < rp32) bt[(tid & 15) * kTLd + (tid >> 4) + 32 * e] = bv[e];
-        __syncthreads();   // (the buffers written two tiles ago were read before the last barrier)
+                if (32 * e < rp32) bt[(tid & 15) * ld + (tid >> 4) + 32 * e] = bv[e];
+        __syncthreads();
         if (wave == (turn & (kWaves - 1))) {
             i32x4_t s = {0, 0, 0, 0};
 #pragma unroll
@@ -300,8 +304,8 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = (float)s[e] * (sx * a.sw[min(n + e, a.N - 1)]);
             for (int j = 0; j < rp32; j += 32)
-                f = mfma16<DT>(*reinterpret_cast<const u32x4_t*>(bt + i * kTLd + j + 8 * g),
-                               *reinterpret_cast<const u32x4_t*>(tl + i * kTLd + j + 8 * g), f);
+                f = mfma16<DT>(*reinterpret_cast<const u32x4_t*>(bt + i * ld + j + 8 * g),
+                               *reinterpret_cast<const u32x4_t*>(tl + i * ld + j + 8 * g), f);
             if (i < a.M) {
                 uint16_t* o = a.y + (int64_t)i * a.N + n;
                 const u32x2_t v = {pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])};
@@ -325,7 +329,7 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
             i32x4_t xv;
             if constexpr (SELF) {
                 const int s = min(wave + kWaves * (b * D + e), KS - 1);
-                xv = *reinterpret_cast<const i32x4_t*>(lds + kOffX + xoff + 64u * (uint32_t)s);
+                xv = *reinterpret_cast<const i32x4_t*>(lds + xat + xoff + 64u * (uint32_t)s);
             } else {
                 xv = __builtin_bit_cast(i32x4_t, cur.x[e]);
             }
@@ -390,7 +394,7 @@ qlora_status launch_int8_gemv(const uint16_t* x, const int8_t* xq, const float* 
         a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(kProducers * 8));
     }
     const bool self = xq == nullptr;
-    const size_t need = std::max<size_t>(kOffX + (self ? (size_t)M * (K + 16) : 0), a.P ? kWaves * 8 * 64 * 16 : 0);
+    const size_t need = std::max<size_t>(off_x(r) + (self ? (size_t)M * (K + 16) : 0), a.P ? kWaves * 8 * 64 * 16 : 0);
     const unsigned grid = (unsigned)(a.P + std::min(a.tiles, 512));
     with_dt(dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
