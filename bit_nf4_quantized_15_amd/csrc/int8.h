@@ -12,6 +12,8 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // int32 sums of K products of codes stay below 2^31: 128 * 128 * (2^17 - 64) < 2^31.
 constexpr int64_t kInt8MaxK = int64_t(1) << 17;
+// The input gradient's tiles have up to 256 rows of K 16-bit values within 31-bit offsets.
+constexpr int64_t kInt8DxMaxK = int64_t(1) << 22;
 
 // The 16-bit values of the four codes of a dword, two per result word:
 // RNE_16(fl32(scale * code)).  The compiler converts each signed byte in place

@@ -470,8 +470,7 @@ qlora_status run(const uint16_t* dy, const int8_t* wq, const float* sw, const ui
         sp.part = static_cast<uint8_t*>(ws) + align256((size_t)(tiles * splits) * 8);
     }
     const int64_t total = tiles * (SPLIT ? sp.splits : 1);
-    if (total * kThreads >= (int64_t(1) << 32) || (int64_t)gm * tn >= (int64_t(1) << 31) ||
-        (int64_t)kBM * K * 2 >= (int64_t(1) << 31))
+    if (total * kThreads >= (int64_t(1) << 32) || (int64_t)gm * tn >= (int64_t(1) << 31))
         return QLORA_ERR_UNSUPPORTED_SHAPE;
     const bool av = r % 8 == 0;
     with_dt(dt, [&](auto dtc) {

@@ -410,7 +410,8 @@ qlora_status qlora_int8_dequantize(const qlora_int8* q, uint16_t* out, void* str
  *   t = s * (x A)                                     [M, r], s = alpha / r
  *   y[m, n] = RNE_16( sx[m] sw[n] sum_k xq[m,k] wq[n,k] + sum_j t[m,j] B[j,n] )
  * The int8 sum is exact (int32; K < 131072), everything after it is fp32 up to
- * the one rounding of y; t is the 16-bit t that qlora_lora_down defines.
+ * the one rounding of y; t is qlora_lora_down's 16-bit t, its fp32 sums in
+ * another order (the last bit may differ).
  * x_keep (nullable) receives (xq, sx), rows == M, cols == K and the weight's
  * dtype: the activation checkpoint that qlora_lora_grads_batch_int8 takes later,
  * after which x itself can be freed.  r == 0: no LoRA branch (A, B and t_out
@@ -430,8 +431,10 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
  *   u  = s * (dy B^T)            [M, r]  into the caller's u (kept for the gradients)
  *   dx = dy W_16 + u A^T         [M, K],  W_16[n, k] = RNE_16( fl32( sw[n] * wq[n, k] ) )
  * r == 0: dx = dy W_16 (A, B, u NULL).  qlora_int8_gemm_bwd_dx is the dx stage for a
- * given u, with no workspace; it may add dx's fp32 sums in another order than the call
- * above, which splits long reductions of few tokens: dx may differ in the last bit.  M == 0 is a no-op.  Errors as qlora_linear_bwd_dx. */
+ * given u, with no workspace; it may add dx's fp32 sums in another order than the
+ * call above, which splits long reductions of few tokens (the last bit may differ).
+ * M == 0 is a no-op.  Errors as qlora_linear_bwd_dx, plus K >= 2^22 ->
+ * UNSUPPORTED_SHAPE. */
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
 qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
                                       float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
@@ -445,7 +448,8 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
  * x_16[m, k] = RNE_16( fl32( x_scale[m] * x[m, k] ) ), the tensor that
  * qlora_int8_dequantize restores; it is formed in registers, never in memory.
  * dtype is the format of t, u, dy and x_16.  Deterministic.  Arguments, empty
- * layers and errors as qlora_lora_grads_batch, plus K % 64 -> UNSUPPORTED_SHAPE. */
+ * layers and errors as qlora_lora_grads_batch, plus K % 64, or K or N above 2^22 ->
+ * UNSUPPORTED_SHAPE. */
 typedef struct qlora_lora_grads_int8 {
     const int8_t* x;      /* [M, K] codes of the layer's input             */
     const float* x_scale; /* [M]                                           */

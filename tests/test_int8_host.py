@@ -141,6 +141,17 @@ def test_grads_arguments(q):
         assert call(rec(), ws=FAKE + 8) == MISALIGNED
 
 
+def test_sizes_past_the_offsets_of_a_tile(q):
+    """Refused before anything is launched: rows whose tiles pass 31-bit offsets."""
+    w = _st(q, cols=1 << 22)
+    assert q.lib.qlora_int8_linear_bwd_dx(ctypes.byref(w), 4, FAKE, FAKE, 8, 1.0, FAKE, FAKE, FAKE, FAKE, BIG,
+                                          None) == SHAPE
+    assert q.lib.qlora_int8_gemm_bwd_dx(ctypes.byref(w), FAKE, 4, FAKE, FAKE, 8, FAKE, None) == SHAPE
+    for K, N in (((1 << 22) + 64, 64), (128, (1 << 22) + 1)):
+        one = (q.LoraGradsInt8 * 1)(q.LoraGradsInt8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 70, N, K))
+        assert q.lib.qlora_lora_grads_batch_int8(one, 1, 8, 0, FAKE, BIG, None) == SHAPE
+
+
 def test_workspace_queries_of_bad_sizes(q):
     for a in ((0, 64, 64, 8), (4, 64, 100, 8), (-1, 64, 64, 8), (4, 0, 64, 8), (4, 64, 64, 129), (4, 64, 64, -1)):
         assert int(q.lib.qlora_int8_fwd_workspace(*a)) == 0
