@@ -2,12 +2,13 @@
 // branch's t = RNE_16(s x A) ("bitsandbytes deep dive", section 4: absmax int8 per row;
 // 12.2: the LoRA side path).
 //
-// A workgroup of 8 waves takes 16 or 32 tokens over all of K, so t needs no split sums and a
+// A workgroup of 8 waves takes 2 to 32 tokens over all of K, so t needs no split sums and a
 // row's maximum no second launch; its waves deal the 64-wide steps of K round robin.  Pass 1
 // reads x as MFMA operands (a lane: 16 values of one token), keeps the maxima, and multiplies
 // with A, of which each wave copies its 64 rows (one contiguous run) through LDS of its own
 // and reads them down their columns.  Pass 2 reads the rows again (L2) and writes codes.
-// Bound by A from L2 (2 K r bytes per workgroup) and, above some thousand tokens, by x.
+// Bound by A from L2 (2 K r bytes per workgroup) and, above some thousand tokens, by x:
+// 2048 x 4096, r = 64: 17 us; 8192 x 8192, r = 64: 75 us, 2.7 TB/s of x and codes.
 #include "int8.h"
 
 namespace qlora {
@@ -49,7 +50,7 @@ constexpr int prep_lds() {
 template <int TQ, int NR, bool VEC, int DT>
 __global__ __launch_bounds__(kThreads, 2) void int8_prep_kernel(const uint16_t* __restrict__ x,
                                                                 const uint16_t* __restrict__ A, float s, int M, int K,
-                                                                int r, int8_t* __restrict__ codes,
+                                                                int r, int per, int8_t* __restrict__ codes,
                                                                 float* __restrict__ scale, uint16_t* __restrict__ t) {
     constexpr int kLd = 16 * TQ + 16, kAL = 2 * TQ;        // halves of a staged row of A; 16-byte loads per lane
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -57,8 +58,8 @@ __global__ __launch_bounds__(kThreads, 2) void int8_prep_kernel(const uint16_t* 
     __shared__ RowScale rs[16 * NR];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t m0 = (int64_t)blockIdx.x * 16 * NR;
-    const int rows = (int)min((int64_t)16 * NR, M - m0), KS = K >> 6;
+    const int64_t m0 = (int64_t)blockIdx.x * per;
+    const int rows = (int)min((int64_t)per, M - m0), KS = K >> 6;
     const rsrc_t xrs = buf_rsrc(x + m0 * K, (uint64_t)rows * K * 2);
     const rsrc_t ars = buf_rsrc(A, (uint64_t)K * r * 2);
     const uint32_t xoff = (uint32_t)i * (uint32_t)K * 2u + 32u * g;
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(kThreads, 2) void int8_prep_kernel(const uint16_t* 
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)   // (rows past M lie past the buffer)
+            for (int c = 0; c < 2; ++c)   // (rows past the last lie past the buffer)
                 q.x[n][c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                     xrs, on ? xoff + (uint32_t)(16 * n) * (uint32_t)K * 2u + 128u * (uint32_t)st + 16u * c : kNone, 0, 0));
         // rows 64 st .. of A: 128 r consecutive bytes
@@ -211,12 +212,12 @@ __global__ __launch_bounds__(kThreads, 2) void int8_prep_kernel(const uint16_t* 
 template <int TQ, int DT>
 __global__ __launch_bounds__(kThreads, 2) void int8_u_kernel(const uint16_t* __restrict__ dy,
                                                              const uint16_t* __restrict__ B, float s, int M, int N,
-                                                             int r, uint16_t* __restrict__ u) {
+                                                             int r, int per, uint16_t* __restrict__ u) {
     __shared__ __attribute__((aligned(16))) f32x4_t red[kWaves * TQ * 64];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int rows = (int)min((int64_t)16, M - m0), steps = (N + 63) >> 6;
+    const int64_t m0 = (int64_t)blockIdx.x * per;
+    const int rows = (int)min((int64_t)per, M - m0), steps = (N + 63) >> 6;
     const rsrc_t drs = buf_rsrc(dy + m0 * N, (uint64_t)rows * N * 2);
     const rsrc_t brs = buf_rsrc(B, (uint64_t)r * N * 2);
     struct Step {
@@ -276,19 +277,33 @@ __global__ __launch_bounds__(kThreads, 2) void int8_u_kernel(const uint16_t* __r
 
 }  // namespace
 
-// Up to 1024 tokens and 5120 columns: 300 x 4096, r = 16 (the whole dx call) 46.0 us with
-// split sums and 40.2 here, 512 x 4096, r = 64 65.3 and 58.3; 2048 x 4096 83.2 and 90.7, 1024 x
-// 11008 118.4 and 148.5 (every workgroup reads all of B).
-bool int8_u_supported(int64_t M, int64_t N, int r) { return N % 8 == 0 && N <= 5120 && M <= 1024 && r <= 128; }
+// Tokens per workgroup: with few of them a CU's own rate bounds a workgroup, so it takes
+// fewer tokens (of the MFMA's 16 columns the others multiply zeros) while that fills the chip.
+// The forward of 333 x 11008 -> 4096, r = 8: 50.1 us with 16 tokens each, 39.6 us with 2;
+// 128 x 4096 -> 4096, r = 16: 21.1 and 16.7 us.
+static int rows_per_wg(int M) {
+    int per = 16;
+    while (per > 2 && (M + per / 2 - 1) / (per / 2) <= 256) per /= 2;
+    return per;
+}
+
+// Every workgroup reads all of B, so this pays for few tokens, narrow layers and small ranks.
+// The whole dx call, us, here and with split sums (tokens x N, r): 300 x 4096, 16: 38.1, 46.6;
+// 512 x 4096, 64: 55.2, 64.4; 100 x 11008, 64: 88.3, 106.1; 512 x 11008, 16: 77.6, 80.2; but
+// 777 x 11000, 24: 108.6, 106.6; 512 x 11008, 64: 111.2, 93.3; 64 x 28672, 64: 186.4, 159.6.
+bool int8_u_supported(int64_t M, int64_t N, int r) {
+    return N % 8 == 0 && N <= 16384 && M <= 1024 && M * r * N <= 150000000;
+}
 
 qlora_status launch_int8_u(const uint16_t* dy, const uint16_t* B, float s, int M, int N, int r, uint16_t* u, int dt,
                            hipStream_t st) {
-    const int64_t grid = ((int64_t)M + 15) / 16;
+    const int per = rows_per_wg(M);
+    const int64_t grid = ((int64_t)M + per - 1) / per;
     if (grid * kThreads >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     with_dt(dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
 #define QL_U(TQ) \
-    hipLaunchKernelGGL((int8_u_kernel<TQ, DT>), dim3((unsigned)grid), dim3(kThreads), 0, st, dy, B, s, M, N, r, u)
+    hipLaunchKernelGGL((int8_u_kernel<TQ, DT>), dim3((unsigned)grid), dim3(kThreads), 0, st, dy, B, s, M, N, r, per, u)
         if (r <= 16) QL_U(1);
         else if (r <= 32) QL_U(2);
         else if (r <= 64) QL_U(4);
@@ -305,13 +320,14 @@ qlora_status launch_int8_prep(const uint16_t* x, const uint16_t* A, float s, int
     const bool vec = r % 8 == 0;
     // 32 tokens halve what each reads of A, but only where there are tokens for every CU
     const int nr = tq <= 4 && M > 4096 ? 2 : 1;
-    const int64_t grid = ((int64_t)M + 16 * nr - 1) / (16 * nr);
+    const int per = nr == 2 ? 32 : rows_per_wg(M);
+    const int64_t grid = ((int64_t)M + per - 1) / per;
     if (grid * kThreads >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     with_dt(dt, [&](auto dtc) {
         constexpr int DT = decltype(dtc)::value;
 #define QL_P(TQ, NR, V)                                                                                           \
     hipLaunchKernelGGL((int8_prep_kernel<TQ, NR, V, DT>), dim3((unsigned)grid), dim3(kThreads), (prep_lds<TQ, NR>()), st, x, \
-                       A, s, M, K, r, codes, scale, t)
+                       A, s, M, K, r, per, codes, scale, t)
 #define QL_P1(TQ)                                                        \
     if (nr == 2) { if (vec) QL_P(TQ, 2, true); else QL_P(TQ, 2, false); } \
     else { if (vec) QL_P(TQ, 1, true); else QL_P(TQ, 1, false); }
