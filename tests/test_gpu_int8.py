@@ -6,6 +6,8 @@ each rounding to it (of the output, and of t or u where the formula goes through
 the smallest subnormal more for fp16), and for fp32 sums of n products, in whatever order,
 (n + 8) 2^-23 of the sum of their magnitudes.  Outputs start as NaN (tests/conftest.py).
 """
+import math
+
 import numpy as np
 import pytest
 
@@ -387,3 +389,34 @@ def test_offsets_past_32_bits(q):
     want = torch.mm(small.codes.double() * small.scale.double()[:, None],
                     (wsm.codes.double() * wsm.scale.double()[:, None]).t().contiguous())
     assert bool(((y[rows].double() - want).abs() <= want.abs() * (h + 2.0 ** -20)).all())
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 65, 64, 3), (13, 200, 320, 24), (33, 257, 192, 7), (70, 136, 704, 64),
+                                     (300, 520, 448, 128), (530, 264, 1152, 16)])
+def test_nothing_is_written_behind_an_output(q, M, N, K, r):
+    """Every output lies inside a larger buffer, which keeps its values on both sides."""
+    import torch
+    say(f"[int8] buffers around the outputs {(M, N, K, r)}")
+    L = Layer(q, "bf16", 9100 + M, M, N, K, r)
+    held = []
+
+    def inside(dtype, *shape):
+        n, pad = math.prod(shape), 4096
+        buf = torch.full((n + 2 * pad,), 77, dtype=dtype, device="cuda:0")
+        held.append((buf, pad, n))
+        return buf[pad:pad + n].view(*shape)
+
+    bf, f32 = torch.bfloat16, torch.float32
+    keep = q.Int8Tensor(inside(torch.int8, M, K), inside(f32, M), bf)
+    y, t, u, dx = inside(bf, M, N), inside(bf, M, r), inside(bf, M, r), inside(bf, M, K)
+    x16, dA, dB = inside(bf, M, K), inside(f32, K, r), inside(f32, r, N)
+    q.int8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha, y=y, t=t, keep=keep)
+    q.int8_dequantize(keep, out=x16)
+    dy = y.clone()
+    q.int8_linear_bwd_dx(L.w, L.A, L.B, L.alpha, dy, u=u, dx=dx)
+    q.lora_grads_batch_int8([(keep, t, u, dy)], dA=[dA], dB=[dB])
+    torch.cuda.synchronize()
+    for i, (buf, pad, n) in enumerate(held):
+        assert bool((buf[:pad] == 77).all()) and bool((buf[pad + n:] == 77).all()), i
+    for v in (y, t, u, dx, x16, dA, dB):
+        assert torch.isfinite(v).all()
