@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kThreads, 2) void int8_u_kernel(const uint16_t* __r
 // 128 x 4096 -> 4096, r = 16: 21.1 and 16.7 us.
 static int rows_per_wg(int M) {
     int per = 16;
-    while (per > 2 && (M + per / 2 - 1) / (per / 2) <= 256) per /= 2;
+    while (per > 2 && M <= 256 * (per / 2)) per /= 2;
     return per;
 }
 
