@@ -14,6 +14,8 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 constexpr int64_t kInt8MaxK = int64_t(1) << 17;
 // The input gradient's tiles have up to 256 rows of K 16-bit values within 31-bit offsets.
 constexpr int64_t kInt8DxMaxK = int64_t(1) << 22;
+// It reads the weight's scales, 4 bytes each, at 31-bit offsets too.
+constexpr int64_t kInt8DxMaxN = int64_t(1) << 29;
 
 // The 16-bit values of the four codes of a dword, two per result word:
 // RNE_16(fl32(scale * code)).  The compiler converts each signed byte in place

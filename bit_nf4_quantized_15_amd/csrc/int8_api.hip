@@ -149,7 +149,7 @@ qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint
     if (st != QLORA_OK) return st;
     const int64_t N = w->rows, K = w->cols;
     if (bad_m(M) || bad_rank(r) || (r && !std::isfinite(alpha))) return QLORA_ERR_INVALID_ARG;
-    if (K >= kInt8DxMaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (K >= kInt8DxMaxK || N >= kInt8DxMaxN) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return QLORA_OK;
     if (!dy || !dx || (r && (!A || !B || !u)) || (!r && (A || B || u))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(A) || !aligned16(B) || !aligned16(dy) || !aligned16(u) || !aligned16(dx))
@@ -173,7 +173,7 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
     const qlora_status st = check_int8(w, 1);
     if (st != QLORA_OK) return st;
     if (bad_m(M) || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
-    if (w->cols >= kInt8DxMaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (w->cols >= kInt8DxMaxK || w->rows >= kInt8DxMaxN) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return QLORA_OK;
     if (!dy || !dx || (r && (!u || !A)) || (!r && (u || A))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(dx) || !aligned16(u) || !aligned16(A)) return QLORA_ERR_MISALIGNED;

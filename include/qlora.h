@@ -433,8 +433,8 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
  * r == 0: dx = dy W_16 (A, B, u NULL).  qlora_int8_gemm_bwd_dx is the dx stage for a
  * given u, with no workspace; it may add dx's fp32 sums in another order than the
  * call above, which splits long reductions of few tokens (the last bit may differ).
- * M == 0 is a no-op.  Errors as qlora_linear_bwd_dx, plus K >= 2^22 ->
- * UNSUPPORTED_SHAPE. */
+ * M == 0 is a no-op.  Errors as qlora_linear_bwd_dx, plus K >= 2^22 or
+ * N >= 2^29 -> UNSUPPORTED_SHAPE. */
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
 qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
                                       float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
