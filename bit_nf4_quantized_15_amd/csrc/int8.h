@@ -12,6 +12,9 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // int32 sums of K products of codes stay below 2^31: 128 * 128 * (2^17 - 64) < 2^31.
 constexpr int64_t kInt8MaxK = int64_t(1) << 17;
+// Rows (tokens, outputs) of a product: kernels count tiles and chunks in 32 bits up to 8208 rows
+// past the last (the decode kernel asks for the row tile after its own, 512 tiles of 16 on).
+constexpr int64_t kInt8MaxRows = (int64_t(1) << 31) - 16384;
 // The input gradient's tiles have up to 256 rows of K 16-bit values within 31-bit offsets.
 constexpr int64_t kInt8DxMaxK = int64_t(1) << 22;
 // It reads the weight's scales, 4 bytes each, at 31-bit offsets too.

@@ -87,7 +87,7 @@ qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64
     if (st != QLORA_OK) return st;
     const int64_t N = w->rows, K = w->cols;
     if (bad_m(M) || bad_rank(r) || (r && !std::isfinite(alpha))) return QLORA_ERR_INVALID_ARG;
-    if (K >= kInt8MaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (K >= kInt8MaxK || N > kInt8MaxRows || M > kInt8MaxRows) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (x_keep) {
         if ((st = check_int8(x_keep, 0)) != QLORA_OK) return st;
         if (x_keep->rows != M || x_keep->cols != K || x_keep->dtype != w->dtype) return QLORA_ERR_INVALID_ARG;
@@ -123,7 +123,7 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
     qlora_status st = check_int8(w, 1);
     if (st != QLORA_OK || (st = check_int8(x, 0)) != QLORA_OK) return st;
     if (x->cols != w->cols || x->dtype != w->dtype || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
-    if (w->cols >= kInt8MaxK) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (w->cols >= kInt8MaxK || w->rows > kInt8MaxRows || x->rows > kInt8MaxRows) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (x->rows == 0) return QLORA_OK;
     if (!y || (r && (!t || !B)) || (!r && (t || B))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(y) || !aligned16(t) || !aligned16(B)) return QLORA_ERR_MISALIGNED;
@@ -149,7 +149,7 @@ qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint
     if (st != QLORA_OK) return st;
     const int64_t N = w->rows, K = w->cols;
     if (bad_m(M) || bad_rank(r) || (r && !std::isfinite(alpha))) return QLORA_ERR_INVALID_ARG;
-    if (K >= kInt8DxMaxK || N >= kInt8DxMaxN) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (K >= kInt8DxMaxK || N >= kInt8DxMaxN || M > kInt8MaxRows) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return QLORA_OK;
     if (!dy || !dx || (r && (!A || !B || !u)) || (!r && (A || B || u))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(A) || !aligned16(B) || !aligned16(dy) || !aligned16(u) || !aligned16(dx))
@@ -173,7 +173,7 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
     const qlora_status st = check_int8(w, 1);
     if (st != QLORA_OK) return st;
     if (bad_m(M) || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
-    if (w->cols >= kInt8DxMaxK || w->rows >= kInt8DxMaxN) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (w->cols >= kInt8DxMaxK || w->rows >= kInt8DxMaxN || M > kInt8MaxRows) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return QLORA_OK;
     if (!dy || !dx || (r && (!u || !A)) || (!r && (u || A))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(dx) || !aligned16(u) || !aligned16(A)) return QLORA_ERR_MISALIGNED;
@@ -215,7 +215,8 @@ qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, in
         if (bad_sizes(g.M, g.N, g.K, r) || !g.dA || !g.dB) return QLORA_ERR_INVALID_ARG;
         // rows of at most 8 MB: the kernel counts what is left of a wave's rows, and the steps in
         // flight past their end, in 32 signed bits
-        if (g.K % kBlock || g.K > (int64_t(1) << 22) || g.N > (int64_t(1) << 22)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        if (g.K % kBlock || g.K > (int64_t(1) << 22) || g.N > (int64_t(1) << 22) || g.M > kInt8MaxRows)
+            return QLORA_ERR_UNSUPPORTED_SHAPE;
         if (!aligned16(g.dA) || !aligned16(g.dB)) return QLORA_ERR_MISALIGNED;
         if (g.M == 0) continue;
         if (!g.x || !g.x_scale || !g.t || !g.u || !g.dy) return QLORA_ERR_INVALID_ARG;

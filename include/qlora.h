@@ -418,7 +418,7 @@ qlora_status qlora_int8_dequantize(const qlora_int8* q, uint16_t* out, void* str
  * NULL; alpha is not used), 1 <= r <= 128 otherwise; t_out is nullable.
  * qlora_int8_gemm_fwd is the product for a given (xq, sx) and t (t, B NULL when
  * r == 0), with no workspace.  M == 0 is a no-op.  Errors as qlora_linear_fwd,
- * plus K >= 131072 -> UNSUPPORTED_SHAPE. */
+ * plus K >= 131072, or M or N above 2^31 - 16384 -> UNSUPPORTED_SHAPE. */
 size_t qlora_int8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r);
 qlora_status qlora_int8_linear_fwd(const qlora_int8* w, const uint16_t* x, int64_t M, const uint16_t* A,
                                    const uint16_t* B, int r, float alpha, uint16_t* y, uint16_t* t_out,
@@ -433,8 +433,8 @@ qlora_status qlora_int8_gemm_fwd(const qlora_int8* w, const qlora_int8* x, const
  * r == 0: dx = dy W_16 (A, B, u NULL).  qlora_int8_gemm_bwd_dx is the dx stage for a
  * given u, with no workspace; it may add dx's fp32 sums in another order than the
  * call above, which splits long reductions of few tokens (the last bit may differ).
- * M == 0 is a no-op.  Errors as qlora_linear_bwd_dx, plus K >= 2^22 or
- * N >= 2^29 -> UNSUPPORTED_SHAPE. */
+ * M == 0 is a no-op.  Errors as qlora_linear_bwd_dx, plus K >= 2^22,
+ * N >= 2^29 or M above 2^31 - 16384 -> UNSUPPORTED_SHAPE. */
 size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
 qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
                                       float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
@@ -448,8 +448,8 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
  * x_16[m, k] = RNE_16( fl32( x_scale[m] * x[m, k] ) ), the tensor that
  * qlora_int8_dequantize restores; it is formed in registers, never in memory.
  * dtype is the format of t, u, dy and x_16.  Deterministic.  Arguments, empty
- * layers and errors as qlora_lora_grads_batch, plus K % 64, or K or N above 2^22 ->
- * UNSUPPORTED_SHAPE. */
+ * layers and errors as qlora_lora_grads_batch, plus K % 64, K or N above 2^22, or
+ * M above 2^31 - 16384 -> UNSUPPORTED_SHAPE. */
 typedef struct qlora_lora_grads_int8 {
     const int8_t* x;      /* [M, K] codes of the layer's input             */
     const float* x_scale; /* [M]                                           */

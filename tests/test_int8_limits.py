@@ -41,3 +41,37 @@ def test_input_gradient_of_too_many_outputs(q, N, r):
     read as zero, or as another row's)."""
     assert _dx(q, _st(q, N), r=r) == SHAPE
     assert _gemm_dx(q, _st(q, N), r=r) == SHAPE
+
+
+LAST = (1 << 31) - 16384          # the largest row count that is accepted
+
+
+@pytest.mark.parametrize("rows", [LAST + 1, (1 << 31) - 1])
+@pytest.mark.parametrize("r", [0, 8])
+def test_row_counts_that_overflow_an_index(q, rows, r):
+    """Tiles and chunks of rows are counted in 32 bits past their last row: the forward's output columns, the
+    decode kernel's row tiles, and every kernel's tokens, up to some 8000 rows further."""
+    small = _st(q, 64)
+    ab = FAKE if r else None
+    for M in (4, 40):                                        # decode and tiled
+        assert _fwd(q, _st(q, rows), M, r) == SHAPE
+        assert q.lib.qlora_int8_gemm_fwd(_st(q, rows), _st(q, M), ab, ab, r, FAKE, None) == SHAPE
+    assert _fwd(q, small, rows, r) == SHAPE
+    assert q.lib.qlora_int8_gemm_fwd(small, _st(q, rows), ab, ab, r, FAKE, None) == SHAPE
+    assert _dx(q, small, rows, r) == SHAPE
+    assert _gemm_dx(q, small, rows, r) == SHAPE
+
+
+@pytest.mark.parametrize("M", [LAST + 1, (1 << 31) - 1])
+def test_gradients_of_too_many_tokens(q, M):
+    """The gradient kernel's last chunk of rows would end past 2^31."""
+    one = (q.LoraGradsInt8 * 1)(q.LoraGradsInt8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, M, 64, 64))
+    assert q.lib.qlora_lora_grads_batch_int8(one, 1, 8, 0, FAKE, BIG, None) == SHAPE
+
+
+def test_the_largest_row_count_passes_the_checks(q):
+    """LAST itself is not refused for its size: the next check, of the workspace, answers."""
+    w = _st(q, LAST)
+    assert q.lib.qlora_int8_linear_fwd(w, FAKE, 4, None, None, 0, 1.0, FAKE, None, None, FAKE, 16, None) == -4
+    one = (q.LoraGradsInt8 * 1)(q.LoraGradsInt8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, LAST, 64, 64))
+    assert q.lib.qlora_lora_grads_batch_int8(one, 1, 8, 0, FAKE, 16, None) == -4
