@@ -95,6 +95,14 @@ __device__ __forceinline__ u32x2_t codes8(u32x4_t v, const RowScale& r) {
     return o;
 }
 
+// ---- sum sx sw in fp32: (sum sx) sw, in this order.
+// Scales of bf16 rows reach from 2^-149 to 2^121, so the product of two may be subnormal, zero
+// or infinite where the sum's is not.  A sum is zero or from 1 to 2^31 in size: sum sx does not
+// fall below sx (and is exact while subnormal), but passes 2^128 where sx does not.  A token
+// with such a scale takes 2^-32 of it, and the product 2^32 at the end.
+constexpr float kLoudScale = 0x1p90f, kLoudDown = 0x1p-32f, kLoudUp = 0x1p32f;
+__device__ __forceinline__ bool loud_scale(float sx) { return __builtin_fabsf(sx) > kLoudScale; }
+
 qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scale, int dt,
                                   hipStream_t s);
 // launch_int8_quantize and t = RNE_16(s x A) [M, r] (1 <= r <= 128) in one launch

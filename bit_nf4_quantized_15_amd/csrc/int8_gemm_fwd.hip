@@ -380,6 +380,12 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void int8_gemm
         }
         __syncthreads();
     }
+    uint64_t loud[MT];   // lanes whose token has a scale above 2^90
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        loud[i] = __builtin_amdgcn_ballot_w64(loud_scale(sxv[i]));
+        if (loud_scale(sxv[i])) sxv[i] *= kLoudDown;
+    }
     const int tj = l32 & 15, tg = l32 >> 4;
     const rsrc_t yrs = buf_rsrc(y + (int64_t)m0 * N, VEC ? (uint64_t)min(M - m0, kBM) * N * 2 : 0);
 #pragma unroll
@@ -396,8 +402,15 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void int8_gemm
             for (int v4 = 0; v4 < 4; ++v4) {
                 const f32x4_t w4 = *reinterpret_cast<const f32x4_t*>(swt + 32 * (NT * wn + j) + 8 * v4 + 4 * h);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[j][4 * v4 + e] = (float)acc[i][j][4 * v4 + e] * (sxv[i] * w4[e]);
+                for (int e = 0; e < 4; ++e) f[j][4 * v4 + e] = (float)acc[i][j][4 * v4 + e] * sxv[i] * w4[e];
             }
+        if (__builtin_expect(loud[i] != 0, 0)) {
+            const float up = (loud[i] >> lane) & 1 ? kLoudUp : 1.0f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) f[j][v] *= up;
+        }
         // t B: rows 16 kk + 8 h .. + 7 of B, column l32 of each tile, by two transposed reads
         auto rank16 = [&](const uint8_t* slot, int kk, u32x4_t a) __attribute__((always_inline)) {
 #pragma unroll

@@ -302,11 +302,13 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
                 for (int e = 0; e < 4; ++e) s[e] += p[e];
             }
             // lane: token i, outputs n0 + 4 g + e
-            const float sx = reinterpret_cast<const float*>(lds + kOffS)[min(i, a.M - 1)];
+            float sx = reinterpret_cast<const float*>(lds + kOffS)[min(i, a.M - 1)];
+            const float up = loud_scale(sx) ? kLoudUp : 1.0f;
+            if (loud_scale(sx)) sx *= kLoudDown;
             const int n = n0 + 4 * g;
             f32x4_t f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = (float)s[e] * (sx * a.sw[min(n + e, a.N - 1)]);
+            for (int e = 0; e < 4; ++e) f[e] = (float)s[e] * sx * a.sw[min(n + e, a.N - 1)] * up;
             for (int j = 0; j < rp32; j += 32)
                 f = mfma16<DT>(*reinterpret_cast<const u32x4_t*>(bt + i * ld + j + 8 * g),
                                *reinterpret_cast<const u32x4_t*>(tl + i * ld + j + 8 * g), f);
