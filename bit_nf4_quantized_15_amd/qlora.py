@@ -555,11 +555,36 @@ def pooled_bwd(w, x, A, B, alpha, g, dy, t=None, need_dx=True, dx=None, dA=None,
     return dx, dA, dB
 
 
-def _stream_of(t, name):
-    """The stream of an int8 call: the current one of the current device, where its tensors have to be."""
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
+def _dev8(t, dtype, name, shape, cur):
+    """_dev, for tensors that have to be on the current device `cur`: all of an int8 call's, which runs on its
+    current stream."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != cur or not t.is_contiguous():
+        _dev(t, dtype, name)
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def _int8_here(q, name, cur):
+    """The state of an Int8Tensor on the current device (its codes and scale are on one device)."""
+    if q.codes.get_device() != cur:
+        raise ValueError(f"{name}: on {q.codes.device}, but the current device is cuda:{cur}")
+    return ctypes.byref(q.state())
+
+
+def _ws8(nbytes, device, ws, cur):
+    """_ws on the current device."""
+    if ws is None:
+        return (None, 0) if nbytes == 0 else (_empty(nbytes, dtype=torch.uint8, device=device), nbytes)
+    if ws.get_device() != cur or not ws.is_contiguous():
+        raise ValueError(f"ws: must be a contiguous tensor on cuda:{cur}")
+    return _ws(nbytes, device, ws)
+
+
+def _stream8(cur):
     return c_vp(torch._C._cuda_getCurrentRawStream(cur))
 
 
@@ -584,9 +609,11 @@ class Int8Tensor:
     def empty(cls, rows, cols, device="cuda", dtype=torch.bfloat16):
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
-        q = cls.__new__(cls)      # (made here: nothing to check)
+        q = cls.__new__(cls)      # (made here: nothing to check but the device)
         q.codes = _empty((rows, cols), dtype=torch.int8, device=device)
         q.scale = _empty((rows,), dtype=torch.float32, device=device)
+        if not q.codes.is_cuda:
+            raise ValueError(f"device: must be a GPU, got {device}")
         q.dtype, q.rows, q.cols = dtype, rows, cols
         return q
 
@@ -599,21 +626,23 @@ def int8_quantize(x, out=None):
     8-bit weight, or an activation checkpoint.  Returns an Int8Tensor."""
     rows, cols = x.shape
     q = Int8Tensor.empty(rows, cols, x.device, x.dtype) if out is None else out
-    _dev(x, q.dtype, "x", (q.rows, q.cols))
-    _check(lib.qlora_int8_quantize(_ptr(x), ctypes.byref(q.state()), _stream_of(x, "x")), "qlora_int8_quantize")
+    cur = torch.cuda.current_device()
+    _dev8(x, q.dtype, "x", (q.rows, q.cols), cur)
+    _check(lib.qlora_int8_quantize(_ptr(x), _int8_here(q, "out", cur), _stream8(cur)), "qlora_int8_quantize")
     return q
 
 
 def int8_dequantize(q, out=None):
     """The 16-bit [rows, cols] tensor that the codes stand for (qlora_int8_dequantize)."""
+    cur = torch.cuda.current_device()
+    st = _int8_here(q, "q", cur)
     o = _empty((q.rows, q.cols), dtype=q.dtype, device=q.codes.device) if out is None else out
-    _dev(o, q.dtype, "out", (q.rows, q.cols))
-    _check(lib.qlora_int8_dequantize(ctypes.byref(q.state()), _ptr(o), _stream_of(q.codes, "q")),
-           "qlora_int8_dequantize")
+    _dev8(o, q.dtype, "out", (q.rows, q.cols), cur)
+    _check(lib.qlora_int8_dequantize(st, _ptr(o), _stream8(cur)), "qlora_int8_dequantize")
     return o
 
 
-def _int8_branch(w, A, B):
+def _int8_branch(w, A, B, cur):
     """Rank of the LoRA branch of an int8 layer, 0 when there is none (A and B None)."""
     if A is None and B is None:
         return 0
@@ -622,8 +651,8 @@ def _int8_branch(w, A, B):
     r = A.shape[1]
     if r == 0:
         raise ValueError("A and B of rank 0: pass None for a layer without a LoRA branch")
-    _dev(A, w.dtype, "A", (w.cols, r))
-    _dev(B, w.dtype, "B", (r, w.rows))
+    _dev8(A, w.dtype, "A", (w.cols, r), cur)
+    _dev8(B, w.dtype, "B", (r, w.rows), cur)
     return r
 
 
@@ -632,24 +661,25 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     product alone.  keep: an Int8Tensor [M, K] that receives x in 8 bits for the backward.  Returns (y, t or
     None)."""
     M = x.shape[0]
-    r = _int8_branch(w, A, B)
+    cur = torch.cuda.current_device()
+    st = _int8_here(w, "w", cur)
+    r = _int8_branch(w, A, B, cur)
     dev = x.device
-    _dev(x, w.dtype, "x", (M, w.cols))
-    stream = _stream_of(x, "x")
-    y = _empty((M, w.rows), dtype=w.dtype, device=dev) if y is None else _dev(y, w.dtype, "y", (M, w.rows))
+    _dev8(x, w.dtype, "x", (M, w.cols), cur)
+    y = _empty((M, w.rows), dtype=w.dtype, device=dev) if y is None else _dev8(y, w.dtype, "y", (M, w.rows), cur)
     if r == 0:
         if t is not None:
             raise ValueError("t: a layer without a LoRA branch has none")
     elif t is not None:
-        _dev(t, w.dtype, "t", (M, r))
+        _dev8(t, w.dtype, "t", (M, r), cur)
     elif want_t:
         t = _empty((M, r), dtype=w.dtype, device=dev)
     if keep is not None and (keep.rows, keep.cols, keep.dtype) != (M, w.cols, w.dtype):
         raise ValueError(f"keep: expected [{M}, {w.cols}] of {w.dtype}")
-    wsb, wsn = _ws(int(lib.qlora_int8_fwd_workspace(M, w.rows, w.cols, r)), dev, ws)
-    _check(lib.qlora_int8_linear_fwd(ctypes.byref(w.state()), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(y),
-                                     _ptr(t), None if keep is None else ctypes.byref(keep.state()), _ptr(wsb), wsn,
-                                     stream), "qlora_int8_linear_fwd")
+    wsb, wsn = _ws8(int(lib.qlora_int8_fwd_workspace(M, w.rows, w.cols, r)), dev, ws, cur)
+    _check(lib.qlora_int8_linear_fwd(st, _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(y), _ptr(t),
+                                     None if keep is None else _int8_here(keep, "keep", cur), _ptr(wsb), wsn,
+                                     _stream8(cur)), "qlora_int8_linear_fwd")
     return y, t
 
 
@@ -660,15 +690,15 @@ def int8_gemm_fwd(w, x, t=None, B=None, y=None):
         raise ValueError("t and B: both or neither")
     if (x.cols, x.dtype) != (w.cols, w.dtype):
         raise ValueError(f"x: expected [M, {w.cols}] of {w.dtype}")
+    cur = torch.cuda.current_device()
+    sw, sx = _int8_here(w, "w", cur), _int8_here(x, "x", cur)
     r = 0 if t is None else t.shape[1]
     if t is not None:
-        _dev(t, w.dtype, "t", (x.rows, r))
-        _dev(B, w.dtype, "B", (r, w.rows))
-    stream = _stream_of(x.codes, "x")
+        _dev8(t, w.dtype, "t", (x.rows, r), cur)
+        _dev8(B, w.dtype, "B", (r, w.rows), cur)
     y = _empty((x.rows, w.rows), dtype=w.dtype, device=x.codes.device) if y is None else \
-        _dev(y, w.dtype, "y", (x.rows, w.rows))
-    _check(lib.qlora_int8_gemm_fwd(ctypes.byref(w.state()), ctypes.byref(x.state()), _ptr(t), _ptr(B), r, _ptr(y),
-                                   stream), "qlora_int8_gemm_fwd")
+        _dev8(y, w.dtype, "y", (x.rows, w.rows), cur)
+    _check(lib.qlora_int8_gemm_fwd(sw, sx, _ptr(t), _ptr(B), r, _ptr(y), _stream8(cur)), "qlora_int8_gemm_fwd")
     return y
 
 
@@ -676,18 +706,19 @@ def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
     """(u, dx) of the int8 layer for upstream dy (qlora_int8_linear_bwd_dx): u = (alpha/r) dy B^T, kept for
     lora_grads_batch_int8, and dx = dy W + u A^T; A = B = None: (None, dy W)."""
     M = dy.shape[0]
-    r = _int8_branch(w, A, B)
+    cur = torch.cuda.current_device()
+    st = _int8_here(w, "w", cur)
+    r = _int8_branch(w, A, B, cur)
     dev = dy.device
-    _dev(dy, w.dtype, "dy", (M, w.rows))
-    stream = _stream_of(dy, "dy")
+    _dev8(dy, w.dtype, "dy", (M, w.rows), cur)
     if r:
-        u = _empty((M, r), dtype=w.dtype, device=dev) if u is None else _dev(u, w.dtype, "u", (M, r))
+        u = _empty((M, r), dtype=w.dtype, device=dev) if u is None else _dev8(u, w.dtype, "u", (M, r), cur)
     elif u is not None:
         raise ValueError("u: a layer without a LoRA branch has none")
-    dx = _empty((M, w.cols), dtype=w.dtype, device=dev) if dx is None else _dev(dx, w.dtype, "dx", (M, w.cols))
-    wsb, wsn = _ws(int(lib.qlora_int8_linear_bwd_dx_workspace(M, w.rows, w.cols, r)), dev, ws)
-    _check(lib.qlora_int8_linear_bwd_dx(ctypes.byref(w.state()), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(dy),
-                                        _ptr(u), _ptr(dx), _ptr(wsb), wsn, stream), "qlora_int8_linear_bwd_dx")
+    dx = _empty((M, w.cols), dtype=w.dtype, device=dev) if dx is None else _dev8(dx, w.dtype, "dx", (M, w.cols), cur)
+    wsb, wsn = _ws8(int(lib.qlora_int8_linear_bwd_dx_workspace(M, w.rows, w.cols, r)), dev, ws, cur)
+    _check(lib.qlora_int8_linear_bwd_dx(st, M, _ptr(A), _ptr(B), r, float(alpha), _ptr(dy), _ptr(u), _ptr(dx),
+                                        _ptr(wsb), wsn, _stream8(cur)), "qlora_int8_linear_bwd_dx")
     return u, dx
 
 
@@ -697,15 +728,16 @@ def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None):
         raise ValueError("u and A: both or neither")
     M = dy.shape[0]
     r = 0 if u is None else u.shape[1]
-    _dev(dy, w.dtype, "dy", (M, w.rows))
+    cur = torch.cuda.current_device()
+    st = _int8_here(w, "w", cur)
+    _dev8(dy, w.dtype, "dy", (M, w.rows), cur)
     if u is not None:
-        _dev(u, w.dtype, "u", (M, r))
-        _dev(A, w.dtype, "A", (w.cols, r))
-    stream = _stream_of(dy, "dy")
+        _dev8(u, w.dtype, "u", (M, r), cur)
+        _dev8(A, w.dtype, "A", (w.cols, r), cur)
     dx = _empty((M, w.cols), dtype=w.dtype, device=dy.device) if dx is None else \
-        _dev(dx, w.dtype, "dx", (M, w.cols))
-    _check(lib.qlora_int8_gemm_bwd_dx(ctypes.byref(w.state()), _ptr(dy), M, _ptr(u), _ptr(A), r, _ptr(dx),
-                                      stream), "qlora_int8_gemm_bwd_dx")
+        _dev8(dx, w.dtype, "dx", (M, w.cols), cur)
+    _check(lib.qlora_int8_gemm_bwd_dx(st, _ptr(dy), M, _ptr(u), _ptr(A), r, _ptr(dx), _stream8(cur)),
+           "qlora_int8_gemm_bwd_dx")
     return dx
 
 
@@ -722,25 +754,27 @@ def lora_grads_batch_int8(layers, dA=None, dB=None, ws=None):
     dB = [None] * n if dB is None else list(dB)
     if len(dA) != n or len(dB) != n:
         raise ValueError("dA and dB: one tensor per layer")
+    cur = torch.cuda.current_device()
     descs = (LoraGradsInt8 * n)()
     for i, (x, t, u, dy) in enumerate(layers):
         if x.dtype != dt:
             raise TypeError(f"x: expected {dt}, got {x.dtype}")
         M, K = x.rows, x.cols
         N = dy.shape[1]
-        _dev(t, dt, "t", (M, r))
-        _dev(u, dt, "u", (M, r))
-        _dev(dy, dt, "dy", (M, N))
-        stream = _stream_of(x.codes, "x")
+        if x.codes.get_device() != cur:
+            _int8_here(x, "x", cur)      # (raises)
+        _dev8(t, dt, "t", (M, r), cur)
+        _dev8(u, dt, "u", (M, r), cur)
+        _dev8(dy, dt, "dy", (M, N), cur)
         dev = dy.device
         dA[i] = _empty((K, r), dtype=torch.float32, device=dev) if dA[i] is None else \
-            _dev(dA[i], torch.float32, "dA", (K, r))
+            _dev8(dA[i], torch.float32, "dA", (K, r), cur)
         dB[i] = _empty((r, N), dtype=torch.float32, device=dev) if dB[i] is None else \
-            _dev(dB[i], torch.float32, "dB", (r, N))
+            _dev8(dB[i], torch.float32, "dB", (r, N), cur)
         descs[i] = LoraGradsInt8(x.codes.data_ptr(), x.scale.data_ptr(), t.data_ptr(), u.data_ptr(), dy.data_ptr(),
                                  dA[i].data_ptr(), dB[i].data_ptr(), M, N, K)
-    wsb, wsn = _ws(int(lib.qlora_lora_grads_batch_int8_workspace(descs, n, r)), dev, ws)
-    _check(lib.qlora_lora_grads_batch_int8(descs, n, r, DTYPES[dt], _ptr(wsb), wsn, stream),
+    wsb, wsn = _ws8(int(lib.qlora_lora_grads_batch_int8_workspace(descs, n, r)), dev, ws, cur)
+    _check(lib.qlora_lora_grads_batch_int8(descs, n, r, DTYPES[dt], _ptr(wsb), wsn, _stream8(cur)),
            "qlora_lora_grads_batch_int8")
     return dA, dB
 
