@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.h"
+#include "int8_plan.h"
 
 namespace qlora {
 
@@ -108,8 +109,7 @@ qlora_status launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols,
 // launch_int8_quantize and t = RNE_16(s x A) [M, r] (1 <= r <= 128) in one launch
 qlora_status launch_int8_prep(const uint16_t* x, const uint16_t* A, float s, int M, int K, int r, int8_t* codes,
                               float* scale, uint16_t* t, int dt, hipStream_t st);
-// u = RNE_16(s dy B^T) [M, r] without split sums, for sizes where that is faster
-bool int8_u_supported(int64_t M, int64_t N, int r);
+// u = RNE_16(s dy B^T) [M, r] without split sums, where int8_u_supported
 qlora_status launch_int8_u(const uint16_t* dy, const uint16_t* B, float s, int M, int N, int r, uint16_t* u, int dt,
                            hipStream_t st);
 qlora_status launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int dt,
@@ -124,9 +124,6 @@ qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_
 // (xq null; int8_gemv_quantizes says for which sizes), or its codes xq, sx; t given, or made
 // from x (then not null) and A in the launch, with int8_gemv_workspace(r) bytes of workspace
 // that need no clearing, and stored to t_out (nullable).
-constexpr int kInt8GemvMaxM = 16;
-bool int8_gemv_supported(int64_t M, int64_t N, int64_t K, int r);
-bool int8_gemv_quantizes(int64_t M, int64_t K);
 size_t int8_gemv_workspace(int r);
 qlora_status launch_int8_gemv(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                               const uint16_t* t, const uint16_t* A, const uint16_t* B, float scale, uint16_t* y,

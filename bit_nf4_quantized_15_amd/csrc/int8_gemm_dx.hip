@@ -66,7 +66,7 @@ __device__ __forceinline__ u32x4_t load8(const uint16_t* __restrict__ p, int64_t
     return v;
 }
 
-constexpr int kStep = 64;   // rows n per step
+constexpr int kStep = kDxStep;   // rows n per step
 constexpr int kKK = 4;      // MFMA depths (16 n) of a step
 constexpr int kWaves = 4, kThreads = 256;
 
@@ -491,55 +491,10 @@ qlora_status run(const uint16_t* dy, const int8_t* wq, const float* sw, const ui
     return launch_status();
 }
 
-enum { k256x256, k128x256, k128x128, k64x128 };
-struct Choice {
-    int tile, splits;
-};
-inline int64_t tiles_of(int64_t M, int64_t K, int bm, int bk) { return ((M + bm - 1) / bm) * ((K + bk - 1) / bk); }
-
-// Direct loads of dy: whole 16-byte chunks, a panel's offsets within a buffer's 31 bits.
-inline bool direct_dy(int64_t N) { return N % 8 == 0 && 512 * N < (int64_t(1) << 31); }
-
-// The tile (tokens x columns), and the split of the reduction, with the least estimated time
-// in microseconds: a round of n tiles on the 256 CUs takes a start and end plus, per 64 n,
-// the larger of a lone tile's time and its share of what the chip sustains.  Measured (the
-// product alone; tokens x N x K):
-//                        256x256  128x256  128x128  64x128
-//   4096 x 11008 x 4096    300.0    351.3    423.2   489.6
-//   2048 x 4096 x 4096      87.4     72.5     86.7    98.3
-//   777 x 11000 x 4096     234.8    140.5    101.4   115.0
-//   300 x 4096 x 4096       81.3     54.0     36.4    30.0
-Choice choose(int64_t M, int64_t N, int64_t K, bool may_split) {
-    const double steps = (double)((N + kStep - 1) / kStep);
-    auto rounds = [&](int64_t n, double s, double ends, double tile_us, double chip_us) {
-        const double last = (double)(n % 256);
-        return (double)(n / 256) * (ends + s * chip_us) +
-               (last > 0 ? ends + s * std::max(tile_us, chip_us * last / 256) : 0.0);
-    };
-    Choice best{k128x128, 1};
-    double us = rounds(tiles_of(M, K, 128, 128), steps, 4.0, 0.47, 0.60);
-    auto offer = [&](double t, int tile, int splits) {
-        if (t < us) {
-            us = t;
-            best = Choice{tile, splits};
-        }
-    };
-    offer(rounds(tiles_of(M, K, 64, 128), steps, 3.0, 0.39, 0.39), k64x128, 1);
-    if (!direct_dy(N)) return best;
-    offer(rounds(tiles_of(M, K, 256, 256), steps, 9.0, 1.15, 1.72), k256x256, 1);
-    const int64_t n = tiles_of(M, K, 128, 256);
-    offer(rounds(n, steps, 4.0, 0.74, 1.03), k128x256, 1);
-    // a split adds a partial tile of 128 KB, written and read, and the wait for it
-    if (may_split)
-        for (int s = 2; s <= 8 && n * s <= 256 && steps >= 4 * s; ++s)
-            offer(rounds(n * s, steps / s, 4.0, 0.74, 1.03) + 4.0 + s, k128x256, s);
-    return best;
-}
-
 }  // namespace
 
 size_t int8_gemm_dx_workspace(int64_t M, int64_t N, int64_t K) {
-    const Choice c = choose(M, N, K, true);
+    const Int8Choice c = int8_dx_choice(M, N, K, true);
     if (c.splits == 1) return 0;
     const int64_t tiles = tiles_of(M, K, 128, 256);
     return align256((size_t)(tiles * c.splits) * 8) + (size_t)(tiles * (c.splits - 1)) * 128 * 256 * 4;
@@ -549,13 +504,13 @@ qlora_status launch_int8_gemm_bwd_dx(const uint16_t* dy, const int8_t* wq, const
                                      const uint16_t* A, uint16_t* dx, int M, int N, int K, int r, int dt, void* ws,
                                      hipStream_t s) {
     const bool dyv = direct_dy(N);
-    const Choice c = choose(M, N, K, ws != nullptr);
+    const Int8Choice c = int8_dx_choice(M, N, K, ws != nullptr);
     switch (c.tile) {
-        case k256x256: return run<8, 2, 2, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
-        case k128x256:
+        case kDx256x256: return run<8, 2, 2, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
+        case kDx128x256:
             return c.splits > 1 ? run<4, 2, 4, true>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, c.splits, ws, s)
                                 : run<4, 2, 4, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
-        case k128x128: return run<4, 1, 4, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
+        case kDx128x128: return run<4, 1, 4, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
         default: return run<2, 1, 4, false>(dy, wq, sw, u, A, dx, M, N, K, r, dt, dyv, 1, nullptr, s);
     }
 }

@@ -515,59 +515,10 @@ qlora_status run(const Args& a, int splits, void* ws) {
     return launch_status();
 }
 
-enum { k256x256, k256x192, k128x128, k64x64 };
-struct Choice {
-    int tile, splits;
-};
-
-inline int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
-
-// The tile, and the split of the reduction, with the least estimated time in microseconds.
-// A round of n tiles on the 256 CUs takes a start and end plus, per 64 k, the larger of a
-// tile's MFMA time and its share of what the chip sustains; fitted to measurements of the
-// products below (K = 4096 unless given, quantization of x included):
-//   M x N           256x256  256x192  128x128  128x128 split 2  64x64
-//   4096 x 4096        67.8     88.0     84.6           99.2      138
-//   2048 x 11008      101.9     92.1    111.7                     179
-//   1024 x 4096        48.0     41.6     26.8           30.4
-//   512 x 4096                           21.1           21.1     25.1
-//   333 x 4096, K = 11008                40.5           31.0     53.9
-//   100 x 11008                          19.7           19.2     20.9
-//   128 x 4096                           17.0                    13.2
-//   33 x 4096                            17.1           16.5     11.3
-Choice choose(int64_t M, int64_t N, int64_t K, bool may_split) {
-    const double steps = (double)K / 64;
-    auto rounds = [&](int64_t n, double ends, double tile_us, double chip_us) {
-        const double last = (double)(n % 256);
-        return (double)(n / 256) * (ends + steps * chip_us) +
-               (last > 0 ? ends + 4.0 + steps * std::max(tile_us, chip_us * last / 256) : 0.0);
-    };
-    Choice best{k256x256, 1};
-    double us = rounds(tiles_of(M, N, 256, 256), 9.5, 0.44, 0.80);
-    auto offer = [&](double t, int tile, int splits) {
-        if (t < us) {
-            us = t;
-            best = Choice{tile, splits};
-        }
-    };
-    offer(rounds(tiles_of(M, N, 256, 192), 8.0, 0.34, 0.62), k256x192, 1);
-    const int64_t n128 = tiles_of(M, N, 128, 128), n64 = tiles_of(M, N, 64, 64);
-    auto small = [&](int64_t n, double s) {   // 128 x 128, s steps each
-        const double last = (double)(n % 256);
-        return (double)(n / 256) * (2.5 + s * 0.28) + (last > 0 ? 4.0 + s * (0.12 + 0.16 * last / 256) : 0.0);
-    };
-    offer(small(n128, steps), k128x128, 1);
-    // a split adds a partial tile of 64 KB, written and read, and the wait for it
-    if (may_split && K >= 1024)
-        for (int s = 2; s <= 4 && n128 * s <= 256; ++s) offer(small(n128 * s, steps / s) + 3.0 + s, k128x128, s);
-    offer((double)((n64 + 511) / 512) * 3.0 + steps * (0.04 + 0.0005 * (double)n64), k64x64, 1);
-    return best;
-}
-
 }  // namespace
 
 size_t int8_gemm_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-    const Choice c = choose(M, N, K, true);
+    const Int8Choice c = int8_fwd_choice(M, N, K, true);
     if (c.splits == 1) return 0;
     const int64_t tiles = tiles_of(M, N, 128, 128);
     return align256((size_t)(tiles * c.splits) * 8) + (size_t)(tiles * (c.splits - 1)) * 128 * 128 * 4;
@@ -577,11 +528,11 @@ qlora_status launch_int8_gemm_fwd(const int8_t* xq, const float* sx, const int8_
                                   const uint16_t* t, const uint16_t* B, uint16_t* y, int M, int N, int K, int r, int dt,
                                   void* ws, hipStream_t s) {
     const Args a{xq, sx, wq, sw, t, B, y, M, N, K, r, dt, s};
-    const Choice c = choose(M, N, K, ws != nullptr);
+    const Int8Choice c = int8_fwd_choice(M, N, K, ws != nullptr);
     switch (c.tile) {
-        case k256x256: return run<2, 2, 4, 4, 128, 2, false>(a, 1, nullptr);
-        case k256x192: return run<2, 2, 4, 3, 128, 2, false>(a, 1, nullptr);
-        case k128x128:
+        case kFwd256x256: return run<2, 2, 4, 4, 128, 2, false>(a, 1, nullptr);
+        case kFwd256x192: return run<2, 2, 4, 3, 128, 2, false>(a, 1, nullptr);
+        case kFwd128x128:
             return c.splits > 1 ? run<2, 2, 2, 2, 128, 4, true>(a, c.splits, ws) : run<2, 2, 2, 2, 128, 4, false>(a, 1, nullptr);
         default: return run<2, 2, 1, 1, 64, 8, false>(a, 1, nullptr);
     }

@@ -47,7 +47,6 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
 
 constexpr int kWaves = 8, kThreads = 512, kRows = 16;
 constexpr int kProducers = 8;
-constexpr uint32_t kSelfBytes = 72u << 10;
 
 struct GemvArgs {
     const uint16_t* x;      // 16-bit x: quantized here, and the producers' operand
@@ -358,13 +357,6 @@ __global__ __launch_bounds__(kThreads, 4) void int8_gemv_kernel(const GemvArgs a
 }
 
 }  // namespace
-
-bool int8_gemv_supported(int64_t M, int64_t N, int64_t K, int r) {
-    // (buffer offsets of B and A within 31 bits)
-    return M <= kInt8GemvMaxM && (int64_t)r * N * 2 < (int64_t(1) << 31) && (int64_t)r * K * 2 < (int64_t(1) << 31);
-}
-
-bool int8_gemv_quantizes(int64_t M, int64_t K) { return M * (K + 16) <= (int64_t)kSelfBytes; }
 
 static int rank_pad(int r) { return (r + 15) & ~15; }
 

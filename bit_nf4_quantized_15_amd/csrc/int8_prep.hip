@@ -277,27 +277,9 @@ __global__ __launch_bounds__(kThreads, 2) void int8_u_kernel(const uint16_t* __r
 
 }  // namespace
 
-// Tokens per workgroup: with few of them a CU's own rate bounds a workgroup, so it takes
-// fewer tokens (of the MFMA's 16 columns the others multiply zeros) while that fills the chip.
-// The forward of 333 x 11008 -> 4096, r = 8: 50.1 us with 16 tokens each, 39.6 us with 2;
-// 128 x 4096 -> 4096, r = 16: 21.1 and 16.7 us.
-static int rows_per_wg(int M) {
-    int per = 16;
-    while (per > 2 && M <= 256 * (per / 2)) per /= 2;
-    return per;
-}
-
-// Every workgroup reads all of B, so this pays for few tokens, narrow layers and small ranks.
-// The whole dx call, us, here and with split sums (tokens x N, r): 300 x 4096, 16: 38.1, 46.6;
-// 512 x 4096, 64: 55.2, 64.4; 100 x 11008, 64: 88.3, 106.1; 512 x 11008, 16: 77.6, 80.2; but
-// 777 x 11000, 24: 108.6, 106.6; 512 x 11008, 64: 111.2, 93.3; 64 x 28672, 64: 186.4, 159.6.
-bool int8_u_supported(int64_t M, int64_t N, int r) {
-    return N % 8 == 0 && N <= 16384 && M <= 1024 && M * r * N <= 150000000;
-}
-
 qlora_status launch_int8_u(const uint16_t* dy, const uint16_t* B, float s, int M, int N, int r, uint16_t* u, int dt,
                            hipStream_t st) {
-    const int per = rows_per_wg(M);
+    const int per = int8_rows_per_wg(M);
     const int64_t grid = ((int64_t)M + per - 1) / per;
     if (grid * kThreads >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     with_dt(dt, [&](auto dtc) {
@@ -318,9 +300,7 @@ qlora_status launch_int8_prep(const uint16_t* x, const uint16_t* A, float s, int
     // (K < 131072: a row group's and A's offsets fit 31 bits)
     const int tq = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8;
     const bool vec = r % 8 == 0;
-    // 32 tokens halve what each reads of A, but only where there are tokens for every CU
-    const int nr = tq <= 4 && M > 4096 ? 2 : 1;
-    const int per = nr == 2 ? 32 : rows_per_wg(M);
+    const int per = int8_prep_rows(M, r), nr = per == 32 ? 2 : 1;
     const int64_t grid = ((int64_t)M + per - 1) / per;
     if (grid * kThreads >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     with_dt(dt, [&](auto dtc) {
