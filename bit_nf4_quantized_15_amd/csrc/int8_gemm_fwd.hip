@@ -10,9 +10,9 @@
 // loop of a 256 x 256 tile on an otherwise idle chip a step takes its MFMAs' time (0.44 us
 // per 64 k).  On the whole chip the clock falls to 1.5 - 1.65 GHz, and what a tile moves
 // counts: rows of 128 bytes per step (whole cache lines) measured 6 - 9 % faster than rows
-// of 64 (8192 x 28672 x 8192, r = 0: 1592 to 1475 us, 2.6 POP/s; 128 x 128 tiles 12 - 20 %).  Sums are
-// exact int32; the scales, t B (r more reduction steps of the 16-bit MFMA) and the rounding
-// follow once per tile.
+// of 64 (8192 x 28672 x 8192, r = 0, calls: 1592 to 1475 us; the kernel's trace: 1434 us, 2.7 POP/s;
+// 128 x 128 tiles 12 - 20 %).  Sums are exact int32; the scales, one after the other (int8.h), t B
+// (r more reduction steps of the 16-bit MFMA) and the rounding follow once per tile.
 //
 // W rows are the MFMA's first operand, so a lane holds one token m and groups of four
 // consecutive outputs n: y leaves through LDS in 8-byte writes and 16-byte stores.  t, the

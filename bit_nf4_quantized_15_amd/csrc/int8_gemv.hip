@@ -18,9 +18,11 @@
 // partials in order, after their first row tile's products, while later weights stream.
 // t B runs on the 16-bit MFMA over the same accumulators' layout.
 //
-// Measured (one launch, weights from HBM): 1 token 4096 -> 4096, r = 16: 8.9 us, of which 3.5 are
-// the weight's bytes (t's hand-off and the reduction's end are the rest); 13 tokens 4096 ->
-// 11008, r = 64: 22 us; 4 tokens 8192 -> 28672, r = 16: 52 us, 4.5 TB/s.
+// t is rounded to 16 bits as everywhere (int8_prep.hip), also where the caller keeps none.
+//
+// Traced, weights from HBM: 1 token 4096 -> 4096, r = 16: 9.6 us, of which 3.5 are the weight's
+// bytes (r = 0: 8.7; t's hand-off and the reduction's end are the rest); 13 tokens 4096 -> 11008,
+// r = 64: 22 us; 4 tokens 8192 -> 28672, r = 16: 49 us, 4.8 TB/s.
 #include "int8.h"
 #include "lora_plan.h"
 #include "split_sync.h"

@@ -20,8 +20,8 @@
 // as in the other LoRA products (split_sync.h): the last split adds the others' partial
 // tiles in order, so results do not depend on timing.
 //
-// Bound by HBM: the seven layers of a 7B-size block, 4096 tokens, r = 64: 119 us, 4.2 TB/s of
-// codes and dy; one layer of 500 tokens, 4096 -> 11008, r = 16: 10.5 us, mostly one tile's latency.
+// Bound by HBM: the seven layers of a 7B-size block, 4096 tokens, r = 64, traced: 117 us, 4.2 TB/s of
+// codes and dy; one layer of 500 tokens, 4096 -> 11008, r = 16: 10.6 us, mostly one tile's latency.
 #include <cstring>
 
 #include "int8.h"

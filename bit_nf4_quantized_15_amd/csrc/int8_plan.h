@@ -49,17 +49,19 @@ inline int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm 
 
 // The tile, and the split of the reduction, with the least estimated time in microseconds.
 // A round of n tiles on the 256 CUs takes a start and end plus, per 64 k, the larger of a
-// tile's MFMA time and its share of what the chip sustains; fitted to measurements of the
-// products below (K = 4096 unless given, quantization of x included):
-//   M x N           256x256  256x192  128x128  128x128 split 2  64x64
-//   4096 x 4096        67.8     88.0     84.6           99.2      138
-//   2048 x 11008      101.9     92.1    111.7                     179
-//   1024 x 4096        48.0     41.6     26.8           30.4
-//   512 x 4096                           21.1           21.1     25.1
-//   333 x 4096, K = 11008                40.5           31.0     53.9
-//   100 x 11008                          19.7           19.2     20.9
-//   128 x 4096                           17.0                    13.2
-//   33 x 4096                            17.1           16.5     11.3
+// tile's MFMA time and its share of what the chip sustains.  The constants are fitted to such
+// measurements; with every tile forced in turn (captured calls, r = 0, codes of x included, us; K = 4096
+// unless given):
+//   M x N                   256x256  256x192  128x128  split 2  split 4   64x64
+//   8192 x 28672, K = 8192   1486.9   1602.0   2142.6
+//   4096 x 4096                76.5     88.5     81.0                     134.1
+//   2048 x 11008              100.9     89.4    105.8                     174.8
+//   1024 x 4096                46.6     40.9     24.9     30.1             39.7
+//   512 x 4096                 44.6     39.1     20.9     20.4     25.2    23.2
+//   333 x 4096, K = 11008      97.4     85.6     40.5     31.1     35.9    52.9
+//   100 x 11008                41.4     35.3     18.4     17.8     23.2    19.8
+//   128 x 4096                 41.0     34.4     16.9     16.3     16.3    12.1
+//   33 x 4096                  40.4     33.9     16.0     15.4     15.4    10.1
 inline Int8Choice int8_fwd_choice(int64_t M, int64_t N, int64_t K, bool may_split) {
     const double steps = (double)K / 64;
     auto rounds = [&](int64_t n, double ends, double tile_us, double chip_us) {
@@ -98,13 +100,13 @@ inline bool direct_dy(int64_t N) { return N % 8 == 0 && 512 * N < (int64_t(1) <<
 
 // The tile (tokens x columns), and the split of the reduction, with the least estimated time
 // in microseconds: a round of n tiles on the 256 CUs takes a start and end plus, per 64 n,
-// the larger of a lone tile's time and its share of what the chip sustains.  Measured (the
-// product alone; tokens x N x K):
-//                        256x256  128x256  128x128  64x128
-//   4096 x 11008 x 4096    300.0    351.3    423.2   489.6
-//   2048 x 4096 x 4096      87.4     72.5     86.7    98.3
-//   777 x 11000 x 4096     234.8    140.5    101.4   115.0
-//   300 x 4096 x 4096       81.3     54.0     36.4    30.0
+// the larger of a lone tile's time and its share of what the chip sustains.  With every tile
+// forced in turn (captured calls, r = 0, us; tokens x N x K):
+//                        256x256  128x256  split 2  split 4  128x128  64x128
+//   4096 x 11008 x 4096    276.3    324.8    352.5    401.8    402.4   453.6
+//   2048 x 4096 x 4096      84.6     65.5     75.6     93.4     76.9    88.0
+//   777 x 11000 x 4096     230.7    138.0     89.5     98.9     94.5   107.7
+//   300 x 4096 x 4096       76.9     51.2     35.8     29.1     34.0    28.9
 inline Int8Choice int8_dx_choice(int64_t M, int64_t N, int64_t K, bool may_split) {
     const double steps = (double)((N + kDxStep - 1) / kDxStep);
     auto rounds = [&](int64_t n, double s, double ends, double tile_us, double chip_us) {

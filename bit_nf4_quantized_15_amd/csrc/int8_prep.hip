@@ -7,8 +7,12 @@
 // reads x as MFMA operands (a lane: 16 values of one token), keeps the maxima, and multiplies
 // with A, of which each wave copies its 64 rows (one contiguous run) through LDS of its own
 // and reads them down their columns.  Pass 2 reads the rows again (L2) and writes codes.
-// Bound by A from L2 (2 K r bytes per workgroup) and, above some thousand tokens, by x:
-// 2048 x 4096, r = 64: 17 us; 8192 x 8192, r = 64: 75 us, 2.7 TB/s of x and codes.
+// Bound by A from L2 (2 K r bytes per workgroup) and, above some thousand tokens, by x; traced:
+// 2048 x 4096, r = 64: 15 us; 8192 x 8192, r = 64: 74 us, 2.7 TB/s of x and codes.
+//
+// t is rounded to 16 bits, also where the caller keeps none: the products t B and t^T dy take
+// it as a 16-bit MFMA operand, and y is the same whether t is kept or not.  An fp32 t would
+// take a second operand for its low bits.
 #include "int8.h"
 
 namespace qlora {

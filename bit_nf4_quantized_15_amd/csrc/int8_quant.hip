@@ -25,8 +25,9 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
 }
 
 // Rows of up to 512 W C values: W waves hold a row in registers, C 16-byte chunks per lane,
-// so x is read once (HBM bound: one pass in, half of it out).  8192 x 28672: 133 us alone, 5.3
-// TB/s (a kernel that read the row twice took 182); 77 x 4096: 3 us, a launch and one row's latency.
+// so x is read once (HBM bound: one pass in, half of it out).  8192 x 28672, traced: 133 us where
+// x is another each time, 5.3 TB/s (147 where it is the same; a kernel that read the row twice
+// took 182); 77 x 4096: 3.1 us, a launch and one row's latency.
 template <int W, int C, int DT>
 __global__ __launch_bounds__(kQT) void int8_quantize_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
                                                             int8_t* __restrict__ codes, float* __restrict__ scale) {
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(kQT) void int8_quantize_long_kernel(const uint16_t*
     }
 }
 
-// HBM bound (8192 x 28672: 138 us, 5.1 TB/s).  16 codes per lane; `base` counts 16-code chunks of the whole tensor.
+// HBM bound (8192 x 28672, traced: 139 us, 5.1 TB/s).  16 codes per lane; `base` counts 16-code chunks of the whole tensor.
 constexpr int kDqPer = 1024;  // chunks per workgroup
 template <int DT>
 __global__ __launch_bounds__(256) void int8_dequantize_kernel(const int8_t* __restrict__ codes,
