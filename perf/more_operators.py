@@ -169,8 +169,8 @@ def prepare(case, seed):
 # ---- plain forms
 
 def encode(v, block_rows):
-    """e4m3 codes [m, k] and scale bytes of fp32 v, in blocks of block_rows x 128.  The bytes of a row of blocks
-    are padded with zeros to a multiple of four."""
+    """e4m3 codes [m, k] and scale bytes of fp32 v, in blocks of block_rows x 128.  The bytes lie as the blocks of
+    a weight, those of rows as [block, row]; the last dimension is padded with zeros to a multiple of four."""
     m, k = v.shape
     bm, bk = -(-m // block_rows), -(-k // 128)
     p = torch.nn.functional.pad(v, (0, bk * 128 - k, 0, bm * block_rows - m)).view(bm, block_rows, bk, 128)
@@ -179,13 +179,16 @@ def encode(v, block_rows):
     e = torch.where(frac == 0, -127, e)
     codes = torch.ldexp(p, -e[:, None, :, None]).to(torch.float8_e4m3fn)
     codes = codes.view(bm * block_rows, bk * 128)[:m, :k].contiguous()
-    return codes, torch.nn.functional.pad((e + 127).to(torch.uint8), (0, -bk % 4))
+    e = (e + 127).to(torch.uint8)
+    if block_rows == 1:
+        e = e.t().contiguous()
+    return codes, torch.nn.functional.pad(e, (0, -e.shape[1] % 4))
 
 
 def decode(codes, scale, block_rows):
     """The values that codes stand for, in fp32."""
     m, k = codes.shape
-    e = scale[:, :-(-k // 128)].int() - 127
+    e = (scale[:, :m].t() if block_rows == 1 else scale[:, :-(-k // 128)]).int() - 127
     e = e.repeat_interleave(block_rows, 0)[:m].repeat_interleave(128, 1)[:, :k]
     return torch.ldexp(codes.float(), e)
 
@@ -390,6 +393,7 @@ def exact(case, seed):
     if kind == "quantize":
         rows = 1 if state["rows"] else 128
         e, v = stored(state["x"], rows)
+        e = e.t() if state["rows"] else e
         e = torch.nn.functional.pad(e + 127, (0, -e.shape[1] % 4))
         return {"scale": e.to(torch.uint8), "x": v}
     s = state["scale"]
