@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "common.h"
+#include "dropout.h"
 #include "lora_plan.h"
 
 using namespace qlora;
@@ -293,6 +294,23 @@ qlora_status qlora_fused_gemm_bwd_dx(const qlora_nf4* w, const uint16_t* dy, int
                               (hipStream_t)stream);
 }
 
+qlora_status qlora_fused_gemm_bwd_dx_dropout(const qlora_nf4* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                             const uint16_t* A, int r, const qlora_dropout* drop, uint16_t* dx,
+                                             void* stream) {
+    DropArgs d;
+    if (!drop || !drop_args(drop, &d)) return QLORA_ERR_INVALID_ARG;
+    if (!d.thr) return qlora_fused_gemm_bwd_dx(w, dy, M, u, A, r, dx, stream);
+    const qlora_status st = check_state(w);
+    if (st != QLORA_OK) return st;
+    const int64_t N = w->n, K = w->k;
+    if (bad_dims(M, N, K, r)) return QLORA_ERR_INVALID_ARG;
+    if (M == 0) return QLORA_OK;
+    if (!dy || !u || !A || !dx) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(u) || !aligned16(A) || !aligned16(dx)) return QLORA_ERR_MISALIGNED;
+    return launch_gemm_bwd_dx_dropout(dy, w->codes, w->q8, w->a2, cb_of(w), dt_of(w), u, A, d, dx, (int)M, (int)N,
+                                      (int)K, r, (hipStream_t)stream);
+}
+
 size_t qlora_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r) {
     if (bad_dims(M, N, K, r) || M == 0) return 0;
     return align256(nt_ws_bytes(M, N, r));
@@ -319,6 +337,29 @@ qlora_status qlora_linear_bwd_dx(const qlora_nf4* w, int64_t M, const uint16_t* 
                               s);
 }
 
+qlora_status qlora_linear_bwd_dx_dropout(const qlora_nf4* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                         float alpha, const qlora_dropout* drop, const uint16_t* dy, uint16_t* u,
+                                         uint16_t* dx, void* ws, size_t ws_bytes, void* stream) {
+    DropArgs d;
+    if (!drop || !drop_args(drop, &d)) return QLORA_ERR_INVALID_ARG;
+    if (!d.thr) return qlora_linear_bwd_dx(w, M, A, B, r, alpha, dy, u, dx, ws, ws_bytes, stream);
+    qlora_status st = check_state(w);
+    if (st != QLORA_OK) return st;
+    const int64_t N = w->n, K = w->k;
+    if (bad_dims(M, N, K, r) || !std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
+    if (M == 0) return QLORA_OK;
+    if (!A || !B || !dy || !u || !dx) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(dy) || !aligned16(u) || !aligned16(dx))
+        return QLORA_ERR_MISALIGNED;
+    if (!ws || ws_bytes < qlora_linear_bwd_dx_workspace(M, N, K, r)) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QLORA_ERR_MISALIGNED;
+    hipStream_t s = (hipStream_t)stream;
+    if ((st = launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt_of(w), s)) != QLORA_OK)
+        return st;
+    return launch_gemm_bwd_dx_dropout(dy, w->codes, w->q8, w->a2, cb_of(w), dt_of(w), u, A, d, dx, (int)M, (int)N,
+                                      (int)K, r, s);
+}
+
 size_t qlora_lora_prod_batch_workspace(const qlora_lora_prod* items, int count, int r) {
     if (!items || count <= 0 || r < 1 || r > 128) return 0;
     size_t total = 0;
@@ -330,8 +371,9 @@ size_t qlora_lora_prod_batch_workspace(const qlora_lora_prod* items, int count, 
 }
 
 // t_i = s x_i A_i (y_natural) or u_i = s dy_i B_i^T for every item, in launches of up to 8.
-static qlora_status lora_prod_batch(const qlora_lora_prod* items, int count, int r, float alpha, int dtype,
-                                    bool y_natural, void* ws, size_t ws_bytes, void* stream) {
+// drop (nullable): count of them, on the items' x.
+static qlora_status lora_prod_batch(const qlora_lora_prod* items, const DropArgs* drop, int count, int r, float alpha,
+                                    int dtype, bool y_natural, void* ws, size_t ws_bytes, void* stream) {
     if (count < 0 || r < 1 || r > 128 || !std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
     if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F16) return QLORA_ERR_INVALID_ARG;
     if (count == 0) return QLORA_OK;
@@ -348,26 +390,50 @@ static qlora_status lora_prod_batch(const qlora_lora_prod* items, int count, int
     if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     std::vector<NtDesc> d;
+    std::vector<DropArgs> dd;
     d.reserve((size_t)count);
     size_t off = 0;
     for (int i = 0; i < count; ++i) {
         const qlora_lora_prod& e = items[i];
         if (e.M == 0) continue;
+        if (drop) dd.push_back(drop[i]);
         d.push_back(NtDesc{e.x, e.w, at(ws, off), e.out, alpha / (float)r, (int)e.M, (int)e.C});
         off += align256(nt_ws_bytes(e.M, e.C, r));
     }
     if (d.empty()) return QLORA_OK;
+    if (drop) return launch_nt_batch_dropout(d.data(), dd.data(), (int)d.size(), r, dt_of(dtype), (hipStream_t)stream);
     return launch_nt_batch(d.data(), (int)d.size(), y_natural, r, dt_of(dtype), (hipStream_t)stream);
 }
 
 qlora_status qlora_lora_down_batch(const qlora_lora_prod* items, int count, int r, float alpha, int dtype, void* ws,
                                    size_t ws_bytes, void* stream) {
-    return lora_prod_batch(items, count, r, alpha, dtype, true, ws, ws_bytes, stream);
+    return lora_prod_batch(items, nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
+}
+
+// The generator's arguments of each item; any: whether some item drops anything.
+static bool drops_of(const qlora_dropout* drops, int count, std::vector<DropArgs>& out, bool& any) {
+    any = false;
+    for (int i = 0; i < count; ++i) {
+        DropArgs d;
+        if (!drop_args(drops + i, &d)) return false;
+        any = any || d.thr;
+        out.push_back(d);
+    }
+    return true;
+}
+
+qlora_status qlora_lora_down_batch_dropout(const qlora_lora_prod* items, const qlora_dropout* drops, int count, int r,
+                                           float alpha, int dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (count <= 0) return lora_prod_batch(items, nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
+    std::vector<DropArgs> d;
+    bool any;
+    if (!drops || !drops_of(drops, count, d, any)) return QLORA_ERR_INVALID_ARG;
+    return lora_prod_batch(items, any ? d.data() : nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
 }
 
 qlora_status qlora_lora_u_batch(const qlora_lora_prod* items, int count, int r, float alpha, int dtype, void* ws,
                                 size_t ws_bytes, void* stream) {
-    return lora_prod_batch(items, count, r, alpha, dtype, false, ws, ws_bytes, stream);
+    return lora_prod_batch(items, nullptr, count, r, alpha, dtype, false, ws, ws_bytes, stream);
 }
 
 // Workspace of one layer's two gradient contractions in qlora_lora_grads_batch.
@@ -384,8 +450,8 @@ size_t qlora_lora_grads_batch_workspace(const qlora_lora_grads* layers, int coun
     return total;
 }
 
-qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, int r, int dtype, void* ws,
-                                    size_t ws_bytes, void* stream) {
+static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const DropArgs* drop, int count, int r, int dtype,
+                                     void* ws, size_t ws_bytes, void* stream) {
     if (count < 0 || r < 1 || r > 128) return QLORA_ERR_INVALID_ARG;
     if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F16) return QLORA_ERR_INVALID_ARG;
     if (count == 0) return QLORA_OK;
@@ -404,6 +470,7 @@ qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, i
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
     std::vector<TnDesc> d;
+    std::vector<DropArgs> dd;
     d.reserve(2 * (size_t)count);
     size_t off = 0;
     qlora_status st = QLORA_OK;
@@ -415,12 +482,31 @@ qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, i
             continue;
         }
         // dA [K, r] = x^T u ; dB [r, N] = t^T dy, stored transposed from the [N, r] reduction
+        if (drop) {   // (of x; nothing is dropped of dy)
+            dd.push_back(drop[i]);
+            dd.push_back(DropArgs{0u, 0u, 0u, 0u, 0u, 1.0f});
+        }
         d.push_back(TnDesc{g.x, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1});
         off += align256(tn_ws_bytes(g.M, g.K, r));
         d.push_back(TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N});
         off += align256(tn_ws_bytes(g.M, g.N, r));
     }
+    if (drop) return launch_tn_batch_dropout(d.data(), dd.data(), (int)d.size(), r, dt_of(dtype), s);
     return launch_tn_batch(d.data(), (int)d.size(), r, dt_of(dtype), s);
+}
+
+qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, int r, int dtype, void* ws,
+                                    size_t ws_bytes, void* stream) {
+    return lora_grads_batch(layers, nullptr, count, r, dtype, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_lora_grads_batch_dropout(const qlora_lora_grads* layers, const qlora_dropout* drops, int count,
+                                            int r, int dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (count <= 0) return lora_grads_batch(layers, nullptr, count, r, dtype, ws, ws_bytes, stream);
+    std::vector<DropArgs> d;
+    bool any;
+    if (!drops || !drops_of(drops, count, d, any)) return QLORA_ERR_INVALID_ARG;
+    return lora_grads_batch(layers, any ? d.data() : nullptr, count, r, dtype, ws, ws_bytes, stream);
 }
 
 qlora_status qlora_linear_fwd(const qlora_nf4* w, const uint16_t* x, int64_t M, const uint16_t* A, const uint16_t* B,

@@ -1,0 +1,59 @@
+// Host-side choices of the 8-bit float layer: which kernel, which tile and which split a size
+// takes.  Shared by the launchers, the workspace-size queries and the tests.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "lora_plan.h"
+
+namespace qlora {
+
+constexpr int kFp8Block = 128;
+inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
+
+// ---- preparation (codes and t, or u, in one pass): plan_nt in whole blocks of 128
+inline SplitPlan plan_fp8_prep(int64_t M, int64_t C, int r) {
+    SplitPlan sp = plan_nt(M, C, r);
+    sp.chunk = (sp.chunk + kFp8Block - 1) / kFp8Block * kFp8Block;
+    sp.splits = (int)((C + sp.chunk - 1) / sp.chunk);
+    return sp;
+}
+
+// ---- products
+enum Fp8Tile { kFp8T256x256, kFp8T128x128, kFp8T64x64 };
+struct Fp8Choice {
+    int tile, splits;
+};
+
+// Tokens M x outputs O, reduction C.  The tile, and the split of the reduction, with the least
+// estimated time in microseconds: a round of n tiles on the 256 CUs takes a start and end plus,
+// per block of 128, the larger of a lone tile's time and its share of what the chip sustains.
+inline Fp8Choice fp8_choice(int64_t M, int64_t O, int64_t C, bool may_split) {
+    const double steps = (double)fp8_blocks(C);
+    auto tiles = [&](int b) { return ((M + b - 1) / b) * ((O + b - 1) / b); };
+    auto rounds = [&](int64_t n, double s, double ends, double tile_us, double chip_us) {
+        const double last = (double)(n % 256);
+        return (double)(n / 256) * (ends + s * chip_us) +
+               (last > 0 ? ends + s * std::max(tile_us, chip_us * last / 256) : 0.0);
+    };
+    Fp8Choice best{kFp8T256x256, 1};
+    double us = rounds(tiles(256), steps, 8.0, 0.9, 1.6);
+    auto offer = [&](double t, int tile, int splits) {
+        if (t < us) {
+            us = t;
+            best = Fp8Choice{tile, splits};
+        }
+    };
+    offer(rounds(tiles(128), steps, 4.0, 0.30, 0.56), kFp8T128x128, 1);
+    // a split adds a partial tile of 64 KB, written and read, and the wait for it
+    if (may_split)
+        for (int s = 2; s <= 8 && tiles(128) * s <= 256 && steps >= 4 * s; ++s)
+            offer(rounds(tiles(128) * s, steps / s, 4.0, 0.30, 0.56) + 3.0 + s, kFp8T128x128, s);
+    const int64_t n64 = tiles(64);
+    offer((double)((n64 + 511) / 512) * 3.0 + steps * (0.09 + 0.001 * (double)n64), kFp8T64x64, 1);
+    return best;
+}
+
+}  // namespace qlora

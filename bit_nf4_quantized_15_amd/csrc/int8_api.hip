@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "dropout.h"
 #include "int8.h"
 #include "lora_plan.h"
 
@@ -142,9 +143,10 @@ size_t qlora_int8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r
     return dx_product_ws(M, N, r) + int8_gemm_dx_workspace(M, N, K);
 }
 
-qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
-                                      float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
-                                      size_t ws_bytes, void* stream) {
+// drop (nullable): of u A^T
+static qlora_status int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                       float alpha, const DropArgs* drop, const uint16_t* dy, uint16_t* u, uint16_t* dx,
+                                       void* ws, size_t ws_bytes, void* stream) {
     qlora_status st = check_int8(w, 1);
     if (st != QLORA_OK) return st;
     const int64_t N = w->rows, K = w->cols;
@@ -164,12 +166,30 @@ qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint
                                        : launch_nt(dy, B, false, ws, u, alpha / (float)r, (int)M, (int)N, r, dt, s);
         if (st != QLORA_OK) return st;
     }
-    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt,
-                                   need ? at(ws, dx_product_ws(M, N, r)) : nullptr, s);
+    void* part = need ? at(ws, dx_product_ws(M, N, r)) : nullptr;
+    if (r && drop && drop->thr)
+        return launch_int8_gemm_bwd_dx_dropout(dy, w->codes, w->scale, u, A, *drop, dx, (int)M, (int)N, (int)K, r, dt,
+                                               part, s);
+    return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)N, (int)K, r, dt, part, s);
 }
 
-qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
-                                    const uint16_t* A, int r, uint16_t* dx, void* stream) {
+qlora_status qlora_int8_linear_bwd_dx(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                      float alpha, const uint16_t* dy, uint16_t* u, uint16_t* dx, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    return int8_linear_bwd_dx(w, M, A, B, r, alpha, nullptr, dy, u, dx, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_int8_linear_bwd_dx_dropout(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B,
+                                              int r, float alpha, const qlora_dropout* drop, const uint16_t* dy,
+                                              uint16_t* u, uint16_t* dx, void* ws, size_t ws_bytes, void* stream) {
+    DropArgs d;
+    if (!drop || !drop_args(drop, &d)) return QLORA_ERR_INVALID_ARG;
+    return int8_linear_bwd_dx(w, M, A, B, r, alpha, &d, dy, u, dx, ws, ws_bytes, stream);
+}
+
+
+static qlora_status int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                     const uint16_t* A, int r, const DropArgs* drop, uint16_t* dx, void* stream) {
     const qlora_status st = check_int8(w, 1);
     if (st != QLORA_OK) return st;
     if (bad_m(M) || bad_rank(r)) return QLORA_ERR_INVALID_ARG;
@@ -177,8 +197,24 @@ qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int
     if (M == 0) return QLORA_OK;
     if (!dy || !dx || (r && (!u || !A)) || (!r && (u || A))) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(dx) || !aligned16(u) || !aligned16(A)) return QLORA_ERR_MISALIGNED;
+    if (r && drop && drop->thr)
+        return launch_int8_gemm_bwd_dx_dropout(dy, w->codes, w->scale, u, A, *drop, dx, (int)M, (int)w->rows,
+                                               (int)w->cols, r, dt_of(w->dtype), nullptr, (hipStream_t)stream);
     return launch_int8_gemm_bwd_dx(dy, w->codes, w->scale, u, A, dx, (int)M, (int)w->rows, (int)w->cols, r,
                                    dt_of(w->dtype), nullptr, (hipStream_t)stream);
+}
+
+qlora_status qlora_int8_gemm_bwd_dx(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                    const uint16_t* A, int r, uint16_t* dx, void* stream) {
+    return int8_gemm_bwd_dx(w, dy, M, u, A, r, nullptr, dx, stream);
+}
+
+qlora_status qlora_int8_gemm_bwd_dx_dropout(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                            const uint16_t* A, int r, const qlora_dropout* drop, uint16_t* dx,
+                                            void* stream) {
+    DropArgs d;
+    if (!drop || !drop_args(drop, &d)) return QLORA_ERR_INVALID_ARG;
+    return int8_gemm_bwd_dx(w, dy, M, u, A, r, &d, dx, stream);
 }
 
 // Tiles of one launch of the gradient kernel: the layers [i0, i0 + n) of a batch.

@@ -50,6 +50,17 @@ class LoraGradsInt8(ctypes.Structure):
                 ("M", c_i64), ("N", c_i64), ("K", c_i64)]
 
 
+class DropoutState(ctypes.Structure):
+    """Mirror of struct qlora_dropout."""
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("p", ctypes.c_double)]
+
+
+class Fp8State(ctypes.Structure):
+    """Mirror of struct qlora_fp8."""
+    _fields_ = [("codes", c_vp), ("scale", c_vp), ("rows", c_i64), ("cols", c_i64), ("dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32)]
+
+
 QUANT_TYPES = {"nf4": 0, "fp4": 1}                        # qlora_quant_type: the 4-bit codebook
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # qlora_dtype: the compute dtype
 
@@ -66,6 +77,8 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(NF4State)
     I8 = ctypes.POINTER(Int8State)
+    F8 = ctypes.POINTER(Fp8State)
+    DR = ctypes.POINTER(DropoutState)
     sig = {
         "qlora_version": (ctypes.c_int, []),
         "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -129,6 +142,28 @@ def _load():
         "qlora_lora_grads_batch_int8": (ctypes.c_int, [ctypes.POINTER(LoraGradsInt8), ctypes.c_int, ctypes.c_int,
                                                        ctypes.c_int, c_vp, c_sz, c_vp]),
     }
+    sig.update({
+        "qlora_lora_down_batch_dropout": (ctypes.c_int, [ctypes.POINTER(LoraProd), DR, ctypes.c_int, ctypes.c_int,
+                                                         ctypes.c_float, ctypes.c_int, c_vp, c_sz, c_vp]),
+        "qlora_lora_grads_batch_dropout": (ctypes.c_int, [ctypes.POINTER(LoraGrads), DR, ctypes.c_int, ctypes.c_int,
+                                                          ctypes.c_int, c_vp, c_sz, c_vp]),
+        "qlora_linear_bwd_dx_dropout": (ctypes.c_int, [P, c_i64, c_vp, c_vp, ctypes.c_int, ctypes.c_float, DR, c_vp,
+                                                       c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "qlora_fused_gemm_bwd_dx_dropout": (ctypes.c_int, [P, c_vp, c_i64, c_vp, c_vp, ctypes.c_int, DR, c_vp, c_vp]),
+        "qlora_int8_linear_bwd_dx_dropout": (ctypes.c_int, [I8, c_i64, c_vp, c_vp, ctypes.c_int, ctypes.c_float, DR,
+                                                            c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "qlora_int8_gemm_bwd_dx_dropout": (ctypes.c_int, [I8, c_vp, c_i64, c_vp, c_vp, ctypes.c_int, DR, c_vp, c_vp]),
+        "qlora_fp8_scale_bytes": (c_sz, [c_i64, c_i64, ctypes.c_int]),
+        "qlora_fp8_quantize": (ctypes.c_int, [c_vp, F8, c_vp]),
+        "qlora_fp8_dequantize": (ctypes.c_int, [F8, c_vp, c_vp]),
+        "qlora_fp8_fwd_workspace": (c_sz, [c_i64, c_i64, c_i64, ctypes.c_int]),
+        "qlora_fp8_linear_fwd": (ctypes.c_int, [F8, c_vp, c_i64, c_vp, c_vp, ctypes.c_int, ctypes.c_float, DR, c_vp,
+                                                c_vp, c_vp, c_sz, c_vp]),
+        "qlora_fp8_gemm_fwd": (ctypes.c_int, [F8, F8, c_vp, c_vp, ctypes.c_int, c_vp, c_vp]),
+        "qlora_fp8_linear_bwd_dx_workspace": (c_sz, [c_i64, c_i64, c_i64, ctypes.c_int]),
+        "qlora_fp8_linear_bwd_dx": (ctypes.c_int, [F8, c_i64, c_vp, c_vp, ctypes.c_int, ctypes.c_float, DR, c_vp, c_vp,
+                                                   c_vp, c_vp, c_sz, c_vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name, None)
         if fn is None:
@@ -181,6 +216,43 @@ def _dev(t, dtype, name, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+class Dropout:
+    """Dropout of a LoRA branch's input (struct qlora_dropout): probability p, and the counter-based generator's seed
+    and offset, 64 bits each.  The forward and the backward of a layer are given the same one; layers and steps whose
+    masks are to differ take other offsets or seeds.  p acts as round(65536 p) / 65536."""
+
+    def __init__(self, p, seed=0, offset=0):
+        if not 0.0 <= p < 1.0 or round(p * 65536) > 65535:
+            raise ValueError(f"p: expected 0 <= p < 1 and at most 65535/65536 when rounded, got {p}")
+        for name, v in (("seed", seed), ("offset", offset)):
+            if not 0 <= v < 2 ** 64:
+                raise ValueError(f"{name}: expected 0 <= {name} < 2**64, got {v}")
+        self.p, self.seed, self.offset = float(p), int(seed), int(offset)
+
+    def state(self):
+        return DropoutState(self.seed, self.offset, self.p)
+
+
+def _drops(dropout, n):
+    """The array of n drops of a list whose None entries drop nothing."""
+    if len(dropout) != n:
+        raise ValueError("dropout: one entry per layer (None: no dropout)")
+    return (DropoutState * n)(*[DropoutState(0, 0, 0.0) if d is None else d.state() for d in dropout])
+
+
+def _no_f32(w, what):
+    if w.dtype == torch.float32:
+        raise TypeError(f"{what}: dropout is offered for the 16-bit dtypes")
+
+
+def _here(*tensors):
+    """A call with dropout runs on the current device's stream: its tensors (None: not given) have to be there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{cur}")
 
 
 def sizes(N, K):
@@ -316,8 +388,17 @@ def _ws(nbytes, device, ws):
     return _empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
-def linear_fwd(w, x, A, B, alpha, y=None, t=None, want_t=True, ws=None):
-    """y = x W_hat + (alpha/r)(x A) B (qlora_linear_fwd).  Returns (y, t or None)."""
+def linear_fwd(w, x, A, B, alpha, y=None, t=None, want_t=True, ws=None, dropout=None):
+    """y = x W_hat + (alpha/r)(x A) B (qlora_linear_fwd).  Returns (y, t or None).  With a Dropout the branch takes
+    drop(x) for x (qlora_lora_down_batch_dropout, then qlora_fused_gemm_fwd)."""
+    if dropout is not None:
+        _no_f32(w, "linear_fwd")
+        _here(x, A, B, w.codes, w.q8, w.a2, y, t, ws)
+        _dev(B, w.dtype, "B", (A.shape[1], w.N))
+        _dev(x, w.dtype, "x", (x.shape[0], w.K))
+        _dev(A, w.dtype, "A", (w.K, A.shape[1]))
+        t = lora_down(x, A, alpha, t=t, ws=ws, dropout=dropout)
+        return fused_gemm_fwd(w, x, t, B, y=y), (t if want_t else None)
     M, K = x.shape
     r = A.shape[1]
     _dev(x, w.dtype, "x", (M, w.K))
@@ -364,8 +445,11 @@ def read_probe(buf, sink, variant=0):
            "qlora_read_probe")
 
 
-def lora_down(x, A, alpha, t=None, ws=None):
-    """t = (alpha/r) x A [M, r] in x's dtype, bf16 or fp16 (qlora_lora_down)."""
+def lora_down(x, A, alpha, t=None, ws=None, dropout=None):
+    """t = (alpha/r) x A [M, r] in x's dtype, bf16 or fp16 (qlora_lora_down); with a Dropout, of drop(x)
+    (qlora_lora_down_batch_dropout)."""
+    if dropout is not None:
+        return lora_down_batch([(x, A)], alpha, t=[t], ws=ws, dropout=[dropout])[0]
     M, K = x.shape
     r = A.shape[1]
     dt = x.dtype
@@ -393,8 +477,9 @@ def fused_gemm_fwd(w, x, t, B, y=None):
     return y
 
 
-def fused_gemm_bwd_dx(w, dy, u, A, dx=None):
-    """dx = dy W_hat^T + u A^T (qlora_fused_gemm_bwd_dx), u = (alpha/r) dy B^T given: one kernel launch."""
+def fused_gemm_bwd_dx(w, dy, u, A, dx=None, dropout=None):
+    """dx = dy W_hat^T + u A^T (qlora_fused_gemm_bwd_dx), u = (alpha/r) dy B^T given: one kernel launch.  With a
+    Dropout, dy W_hat^T + drop(u A^T) (qlora_fused_gemm_bwd_dx_dropout)."""
     M = dy.shape[0]
     r = u.shape[1]
     _dev(dy, w.dtype, "dy", (M, w.N))
@@ -402,13 +487,36 @@ def fused_gemm_bwd_dx(w, dy, u, A, dx=None):
     _dev(A, w.dtype, "A", (w.K, r))
     dx = _empty((M, w.K), dtype=w.dtype, device=dy.device) if dx is None else _dev(dx, w.dtype, "dx", (M, w.K))
     st = w.state()
+    if dropout is not None:
+        _no_f32(w, "fused_gemm_bwd_dx")
+        _here(dy, u, A, w.codes, w.q8, w.a2, dx)
+        _check(lib.qlora_fused_gemm_bwd_dx_dropout(ctypes.byref(st), _ptr(dy), M, _ptr(u), _ptr(A), r,
+                                                   ctypes.byref(dropout.state()), _ptr(dx), _stream()),
+               "qlora_fused_gemm_bwd_dx_dropout")
+        return dx
     _check(lib.qlora_fused_gemm_bwd_dx(ctypes.byref(st), _ptr(dy), M, _ptr(u), _ptr(A), r, _ptr(dx), _stream()),
            "qlora_fused_gemm_bwd_dx")
     return dx
 
 
-def linear_bwd(w, x, A, B, alpha, dy, t=None, need_dx=True, dx=None, dA=None, dB=None, ws=None):
-    """(dx, dA, dB) of the layer for upstream dy (qlora_linear_bwd); dx is None when not needed."""
+def linear_bwd(w, x, A, B, alpha, dy, t=None, need_dx=True, dx=None, dA=None, dB=None, ws=None, dropout=None):
+    """(dx, dA, dB) of the layer for upstream dy (qlora_linear_bwd); dx is None when not needed.  With the forward's
+    Dropout: its three stages (u and dx, then the gradients of drop(x); a t not given is computed again)."""
+    if dropout is not None:
+        _no_f32(w, "linear_bwd")
+        _here(x, A, B, dy, t, w.codes, w.q8, w.a2, dx, dA, dB, ws)
+        _dev(x, w.dtype, "x", (x.shape[0], w.K))
+        _dev(A, w.dtype, "A", (w.K, A.shape[1]))
+        _dev(B, w.dtype, "B", (A.shape[1], w.N))
+        _dev(dy, w.dtype, "dy", (x.shape[0], w.N))
+        if need_dx:
+            u, dx = linear_bwd_dx(w, A, B, alpha, dy, dx=dx, ws=ws, dropout=dropout)
+        else:
+            u = lora_u_batch([(dy, B)], alpha, ws=ws)[0]
+        if t is None:
+            t = lora_down(x, A, alpha, ws=ws, dropout=dropout)
+        (dA,), (dB,) = lora_grads_batch([(x, t, u, dy)], dA=[dA], dB=[dB], ws=ws, dropout=[dropout])
+        return (dx if need_dx else None), dA, dB
     M, K = x.shape
     r = A.shape[1]
     _dev(x, w.dtype, "x", (M, w.K))
@@ -431,9 +539,10 @@ def linear_bwd(w, x, A, B, alpha, dy, t=None, need_dx=True, dx=None, dA=None, dB
     return (dx if need_dx else None), dA, dB
 
 
-def linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
+def linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None, dropout=None):
     """(u, dx) of the layer for upstream dy (qlora_linear_bwd_dx): u = (alpha/r) dy B^T, kept for
-    lora_grads_batch, and dx = dy W_hat^T + u A^T."""
+    lora_grads_batch, and dx = dy W_hat^T + u A^T.  With the forward's Dropout, dy W_hat^T + drop(u A^T)
+    (qlora_linear_bwd_dx_dropout)."""
     M = dy.shape[0]
     r = A.shape[1]
     _dev(A, w.dtype, "A", (w.K, r))
@@ -444,15 +553,23 @@ def linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
     dx = _empty((M, w.K), dtype=w.dtype, device=dev) if dx is None else _dev(dx, w.dtype, "dx", (M, w.K))
     wsb, wsn = _ws(int(lib.qlora_linear_bwd_dx_workspace(M, w.N, w.K, r)), dev, ws)
     st = w.state()
+    if dropout is not None:
+        _no_f32(w, "linear_bwd_dx")
+        _here(A, B, dy, w.codes, w.q8, w.a2, u, dx, ws)
+        _check(lib.qlora_linear_bwd_dx_dropout(ctypes.byref(st), M, _ptr(A), _ptr(B), r, float(alpha),
+                                               ctypes.byref(dropout.state()), _ptr(dy), _ptr(u), _ptr(dx), _ptr(wsb),
+                                               wsn, _stream()), "qlora_linear_bwd_dx_dropout")
+        return u, dx
     _check(lib.qlora_linear_bwd_dx(ctypes.byref(st), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(dy), _ptr(u),
                                    _ptr(dx), _ptr(wsb), wsn, _stream()), "qlora_linear_bwd_dx")
     return u, dx
 
 
-def lora_grads_batch(layers, dA=None, dB=None, ws=None):
+def lora_grads_batch(layers, dA=None, dB=None, ws=None, dropout=None):
     """dA = x^T u and dB = t^T dy (fp32) of several layers in one launch per 8 layers
     (qlora_lora_grads_batch).  layers: a list of (x, t, u, dy), all of one rank r and one dtype (bf16 or
-    fp16); dA, dB: optional lists of output tensors.  Returns the lists (dA, dB)."""
+    fp16); dA, dB: optional lists of output tensors.  dropout: optional list of the layers' Dropouts (None entries
+    drop nothing), then dA = drop(x)^T u (qlora_lora_grads_batch_dropout).  Returns the lists (dA, dB)."""
     n = len(layers)
     if n == 0:
         return [], []
@@ -477,11 +594,16 @@ def lora_grads_batch(layers, dA=None, dB=None, ws=None):
         descs[i] = LoraGrads(x.data_ptr(), t.data_ptr(), u.data_ptr(), dy.data_ptr(), dA[i].data_ptr(),
                              dB[i].data_ptr(), M, N, K)
     wsb, wsn = _ws(int(lib.qlora_lora_grads_batch_workspace(descs, n, r)), layers[0][0].device, ws)
+    if dropout is not None:
+        _here(ws, *dA, *dB, *(v for layer in layers for v in layer))
+        _check(lib.qlora_lora_grads_batch_dropout(descs, _drops(dropout, n), n, r, code, _ptr(wsb), wsn, _stream()),
+               "qlora_lora_grads_batch_dropout")
+        return dA, dB
     _check(lib.qlora_lora_grads_batch(descs, n, r, code, _ptr(wsb), wsn, _stream()), "qlora_lora_grads_batch")
     return dA, dB
 
 
-def _lora_prod_batch(fn, name, items, alpha, natural, outs, ws):
+def _lora_prod_batch(fn, name, items, alpha, natural, outs, ws, dropout=None):
     n = len(items)
     if n == 0:
         return []
@@ -497,13 +619,21 @@ def _lora_prod_batch(fn, name, items, alpha, natural, outs, ws):
         outs[i] = _empty((M, r), dtype=dt, device=X.device) if outs[i] is None else _dev(outs[i], dt, "out", (M, r))
         descs[i] = LoraProd(X.data_ptr(), Y.data_ptr(), outs[i].data_ptr(), M, C)
     wsb, wsn = _ws(int(lib.qlora_lora_prod_batch_workspace(descs, n, r)), items[0][0].device, ws)
+    if dropout is not None:
+        _here(ws, *outs, *(v for item in items for v in item))
+        _check(fn(descs, _drops(dropout, n), n, r, float(alpha), code, _ptr(wsb), wsn, _stream()), name)
+        return outs
     _check(fn(descs, n, r, float(alpha), code, _ptr(wsb), wsn, _stream()), name)
     return outs
 
 
-def lora_down_batch(items, alpha, t=None, ws=None):
+def lora_down_batch(items, alpha, t=None, ws=None, dropout=None):
     """t_i = (alpha/r) x_i A_i for items [(x_i, A_i)] in one launch per 8 (qlora_lora_down_batch); each t_i is
-    that of lora_down.  t: optional list of outputs.  Returns the list of t_i."""
+    that of lora_down.  t: optional list of outputs.  dropout: optional list of Dropouts (None entries drop nothing),
+    then t_i = (alpha/r) drop_i(x_i) A_i (qlora_lora_down_batch_dropout).  Returns the list of t_i."""
+    if dropout is not None:
+        return _lora_prod_batch(lib.qlora_lora_down_batch_dropout, "qlora_lora_down_batch_dropout", items, alpha, True, t,
+                                ws, dropout)
     return _lora_prod_batch(lib.qlora_lora_down_batch, "qlora_lora_down_batch", items, alpha, True, t, ws)
 
 
@@ -656,10 +786,19 @@ def _int8_branch(w, A, B, cur):
     return r
 
 
-def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True, keep=None, ws=None):
+def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True, keep=None, ws=None, dropout=None):
     """y = sx sw (xq wq^T) + (alpha/r)(x A) B of an int8 weight (qlora_int8_linear_fwd); A = B = None: the int8
     product alone.  keep: an Int8Tensor [M, K] that receives x in 8 bits for the backward.  Returns (y, t or
-    None)."""
+    None).  With a Dropout the branch takes drop(x) for x (qlora_lora_down_batch_dropout, qlora_int8_quantize,
+    qlora_int8_gemm_fwd)."""
+    if dropout is not None:
+        if A is None or B is None:
+            raise ValueError("dropout: a layer without a LoRA branch has none")
+        cur = torch.cuda.current_device()
+        _int8_branch(w, A, B, cur)
+        _dev8(x, w.dtype, "x", (x.shape[0], w.cols), cur)
+        t = lora_down(x, A, alpha, t=t, ws=ws, dropout=dropout)
+        return int8_gemm_fwd(w, int8_quantize(x, out=keep), t, B, y=y), (t if want_t else None)
     M = x.shape[0]
     cur = torch.cuda.current_device()
     st = _int8_here(w, "w", cur)
@@ -702,9 +841,10 @@ def int8_gemm_fwd(w, x, t=None, B=None, y=None):
     return y
 
 
-def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
+def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None, dropout=None):
     """(u, dx) of the int8 layer for upstream dy (qlora_int8_linear_bwd_dx): u = (alpha/r) dy B^T, kept for
-    lora_grads_batch_int8, and dx = dy W + u A^T; A = B = None: (None, dy W)."""
+    lora_grads_batch_int8, and dx = dy W + u A^T; A = B = None: (None, dy W).  With the forward's Dropout,
+    dy W + drop(u A^T) (qlora_int8_linear_bwd_dx_dropout)."""
     M = dy.shape[0]
     cur = torch.cuda.current_device()
     st = _int8_here(w, "w", cur)
@@ -717,13 +857,21 @@ def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None):
         raise ValueError("u: a layer without a LoRA branch has none")
     dx = _empty((M, w.cols), dtype=w.dtype, device=dev) if dx is None else _dev8(dx, w.dtype, "dx", (M, w.cols), cur)
     wsb, wsn = _ws8(int(lib.qlora_int8_linear_bwd_dx_workspace(M, w.rows, w.cols, r)), dev, ws, cur)
+    if dropout is not None:
+        if r == 0:
+            raise ValueError("dropout: a layer without a LoRA branch has none")
+        _check(lib.qlora_int8_linear_bwd_dx_dropout(st, M, _ptr(A), _ptr(B), r, float(alpha),
+                                                    ctypes.byref(dropout.state()), _ptr(dy), _ptr(u), _ptr(dx),
+                                                    _ptr(wsb), wsn, _stream8(cur)), "qlora_int8_linear_bwd_dx_dropout")
+        return u, dx
     _check(lib.qlora_int8_linear_bwd_dx(st, M, _ptr(A), _ptr(B), r, float(alpha), _ptr(dy), _ptr(u), _ptr(dx),
                                         _ptr(wsb), wsn, _stream8(cur)), "qlora_int8_linear_bwd_dx")
     return u, dx
 
 
-def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None):
-    """dx = dy W + u A^T of an int8 weight, u given (qlora_int8_gemm_bwd_dx); u = A = None: dy W alone."""
+def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None, dropout=None):
+    """dx = dy W + u A^T of an int8 weight, u given (qlora_int8_gemm_bwd_dx); u = A = None: dy W alone.  With a
+    Dropout, dy W + drop(u A^T) (qlora_int8_gemm_bwd_dx_dropout)."""
     if (u is None) != (A is None):
         raise ValueError("u and A: both or neither")
     M = dy.shape[0]
@@ -736,6 +884,12 @@ def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None):
         _dev8(A, w.dtype, "A", (w.cols, r), cur)
     dx = _empty((M, w.cols), dtype=w.dtype, device=dy.device) if dx is None else \
         _dev8(dx, w.dtype, "dx", (M, w.cols), cur)
+    if dropout is not None:
+        if r == 0:
+            raise ValueError("dropout: a layer without a LoRA branch has none")
+        _check(lib.qlora_int8_gemm_bwd_dx_dropout(st, _ptr(dy), M, _ptr(u), _ptr(A), r, ctypes.byref(dropout.state()),
+                                                  _ptr(dx), _stream8(cur)), "qlora_int8_gemm_bwd_dx_dropout")
+        return dx
     _check(lib.qlora_int8_gemm_bwd_dx(st, _ptr(dy), M, _ptr(u), _ptr(A), r, _ptr(dx), _stream8(cur)),
            "qlora_int8_gemm_bwd_dx")
     return dx
@@ -777,6 +931,171 @@ def lora_grads_batch_int8(layers, dA=None, dB=None, ws=None):
     _check(lib.qlora_lora_grads_batch_int8(descs, n, r, DTYPES[dt], _ptr(wsb), wsn, _stream8(cur)),
            "qlora_lora_grads_batch_int8")
     return dA, dB
+
+
+FP8_BLOCK = 128
+
+
+class Fp8Tensor:
+    """Device-resident e4m3 codes [rows, cols] with a power-of-two scale byte for each block (struct qlora_fp8): an
+    8-bit frozen weight [N, K] (block_rows 128), or activations (block_rows 1).  codes is torch.float8_e4m3fn, scale
+    torch.uint8 (E8M0) of scale_shape(rows, cols, block_rows).  dtype (torch.bfloat16 or torch.float16) is the 16-bit
+    format of the tensors it is used with."""
+
+    def __init__(self, codes, scale, dtype=torch.bfloat16, block_rows=FP8_BLOCK):
+        if codes.dim() != 2:
+            raise ValueError("codes: expected two dimensions")
+        _fp8_args(dtype, block_rows)
+        _dev(codes, torch.float8_e4m3fn, "codes")
+        _dev(scale, torch.uint8, "scale", self.scale_shape(*codes.shape, block_rows))
+        if scale.device != codes.device:
+            raise ValueError("codes and scale are on different devices")
+        self.codes, self.scale, self.dtype, self.block_rows = codes, scale, dtype, block_rows
+        self.rows, self.cols = codes.shape
+
+    @staticmethod
+    def scale_shape(rows, cols, block_rows=FP8_BLOCK):
+        """Shape of the scale bytes: [row of blocks, block] of a weight, [block, row] of activations, the last
+        dimension rounded up to a multiple of 4."""
+        blocks = -(-cols // FP8_BLOCK)
+        if block_rows == 1:
+            return blocks, -(-rows // 4) * 4
+        return -(-rows // FP8_BLOCK), -(-blocks // 4) * 4
+
+    @classmethod
+    def empty(cls, rows, cols, device="cuda", dtype=torch.bfloat16, block_rows=FP8_BLOCK):
+        _fp8_args(dtype, block_rows)
+        q = cls.__new__(cls)      # (made here: nothing to check but the device)
+        q.codes = _empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
+        q.scale = _empty(cls.scale_shape(rows, cols, block_rows), dtype=torch.uint8, device=device)
+        if not q.codes.is_cuda:
+            raise ValueError(f"device: must be a GPU, got {device}")
+        q.dtype, q.block_rows, q.rows, q.cols = dtype, block_rows, rows, cols
+        return q
+
+    def state(self):
+        return Fp8State(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, DTYPES[self.dtype],
+                        self.block_rows)
+
+
+def _fp8_args(dtype, block_rows):
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
+
+
+def _fp8_quantize(x, out, block_rows):
+    rows, cols = x.shape
+    q = Fp8Tensor.empty(rows, cols, x.device, x.dtype, block_rows) if out is None else out
+    if q.block_rows != block_rows:
+        raise ValueError(f"out: expected block_rows {block_rows}, got {q.block_rows}")
+    cur = torch.cuda.current_device()
+    _dev8(x, q.dtype, "x", (q.rows, q.cols), cur)
+    _check(lib.qlora_fp8_quantize(_ptr(x), _int8_here(q, "out", cur), _stream8(cur)), "qlora_fp8_quantize")
+    return q
+
+
+def fp8_quantize(W, out=None):
+    """e4m3 codes and a power-of-two scale for each 128 x 128 block of a bf16 or fp16 [N, K] device weight
+    (qlora_fp8_quantize).  Returns an Fp8Tensor."""
+    return _fp8_quantize(W, out, FP8_BLOCK)
+
+
+def fp8_quantize_rows(x, out=None):
+    """The same for activations [M, K], in blocks of 128 along each row: the x of fp8_gemm_fwd."""
+    return _fp8_quantize(x, out, 1)
+
+
+def fp8_dequantize(q, out=None):
+    """The 16-bit [rows, cols] tensor that the codes stand for (qlora_fp8_dequantize)."""
+    cur = torch.cuda.current_device()
+    st = _int8_here(q, "q", cur)
+    o = _empty((q.rows, q.cols), dtype=q.dtype, device=q.codes.device) if out is None else out
+    _dev8(o, q.dtype, "out", (q.rows, q.cols), cur)
+    _check(lib.qlora_fp8_dequantize(st, _ptr(o), _stream8(cur)), "qlora_fp8_dequantize")
+    return o
+
+
+def _fp8_weight(w, cur):
+    if w.block_rows != FP8_BLOCK:
+        raise ValueError(f"w: expected a weight (block_rows {FP8_BLOCK})")
+    return _int8_here(w, "w", cur)
+
+
+def _drop_ref(dropout, r):
+    if dropout is None:
+        return None
+    if r == 0:
+        raise ValueError("dropout: a layer without a LoRA branch has none")
+    return ctypes.byref(dropout.state())
+
+
+def fp8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True, ws=None, dropout=None):
+    """y = xq Wq^T + (alpha/r)(x A) B of an fp8 weight, xq the 8-bit x (qlora_fp8_linear_fwd); A = B = None: the fp8
+    product alone.  With a Dropout the branch takes drop(x) for x.  Returns (y, t or None)."""
+    M = x.shape[0]
+    cur = torch.cuda.current_device()
+    st = _fp8_weight(w, cur)
+    r = _int8_branch(w, A, B, cur)
+    drop = _drop_ref(dropout, r)
+    dev = x.device
+    _dev8(x, w.dtype, "x", (M, w.cols), cur)
+    y = _empty((M, w.rows), dtype=w.dtype, device=dev) if y is None else _dev8(y, w.dtype, "y", (M, w.rows), cur)
+    if r == 0:
+        if t is not None:
+            raise ValueError("t: a layer without a LoRA branch has none")
+    elif t is not None:
+        _dev8(t, w.dtype, "t", (M, r), cur)
+    elif want_t:
+        t = _empty((M, r), dtype=w.dtype, device=dev)
+    wsb, wsn = _ws8(int(lib.qlora_fp8_fwd_workspace(M, w.rows, w.cols, r)), dev, ws, cur)
+    _check(lib.qlora_fp8_linear_fwd(st, _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha), drop, _ptr(y), _ptr(t), _ptr(wsb),
+                                    wsn, _stream8(cur)), "qlora_fp8_linear_fwd")
+    return y, t
+
+
+def fp8_gemm_fwd(w, x, t=None, B=None, y=None):
+    """y = xq Wq^T + t B for x given as an Fp8Tensor of block_rows 1 (qlora_fp8_gemm_fwd), for layers that share it;
+    t = B = None: the product alone."""
+    if (t is None) != (B is None):
+        raise ValueError("t and B: both or neither")
+    if (x.cols, x.dtype, x.block_rows) != (w.cols, w.dtype, 1):
+        raise ValueError(f"x: expected [M, {w.cols}] of {w.dtype} in blocks of one row")
+    cur = torch.cuda.current_device()
+    sw, sx = _fp8_weight(w, cur), _int8_here(x, "x", cur)
+    r = 0 if t is None else t.shape[1]
+    if t is not None:
+        if r == 0:
+            raise ValueError("t and B of rank 0: pass None for a layer without a LoRA branch")
+        _dev8(t, w.dtype, "t", (x.rows, r), cur)
+        _dev8(B, w.dtype, "B", (r, w.rows), cur)
+    y = _empty((x.rows, w.rows), dtype=w.dtype, device=x.codes.device) if y is None else \
+        _dev8(y, w.dtype, "y", (x.rows, w.rows), cur)
+    _check(lib.qlora_fp8_gemm_fwd(sw, sx, _ptr(t), _ptr(B), r, _ptr(y), _stream8(cur)), "qlora_fp8_gemm_fwd")
+    return y
+
+
+def fp8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None, dropout=None):
+    """(u, dx) of the fp8 layer for upstream dy (qlora_fp8_linear_bwd_dx): u = (alpha/r) dy B^T, kept for
+    lora_grads_batch, and dx = dyq Wq + u A^T, dyq the 8-bit dy; with the forward's Dropout dyq Wq + drop(u A^T).
+    A = B = None: (None, dyq Wq)."""
+    M = dy.shape[0]
+    cur = torch.cuda.current_device()
+    st = _fp8_weight(w, cur)
+    r = _int8_branch(w, A, B, cur)
+    drop = _drop_ref(dropout, r)
+    dev = dy.device
+    _dev8(dy, w.dtype, "dy", (M, w.rows), cur)
+    if r:
+        u = _empty((M, r), dtype=w.dtype, device=dev) if u is None else _dev8(u, w.dtype, "u", (M, r), cur)
+    elif u is not None:
+        raise ValueError("u: a layer without a LoRA branch has none")
+    dx = _empty((M, w.cols), dtype=w.dtype, device=dev) if dx is None else _dev8(dx, w.dtype, "dx", (M, w.cols), cur)
+    wsb, wsn = _ws8(int(lib.qlora_fp8_linear_bwd_dx_workspace(M, w.rows, w.cols, r)), dev, ws, cur)
+    _check(lib.qlora_fp8_linear_bwd_dx(st, M, _ptr(A), _ptr(B), r, float(alpha), drop, _ptr(dy), _ptr(u), _ptr(dx),
+                                       _ptr(wsb), wsn, _stream8(cur)), "qlora_fp8_linear_bwd_dx")
+    return u, dx
 
 
 def declared_symbols():

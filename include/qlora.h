@@ -465,6 +465,128 @@ size_t qlora_lora_grads_batch_int8_workspace(const qlora_lora_grads_int8* layers
 qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, int count, int r, int dtype, void* ws,
                                          size_t ws_bytes, void* stream);
 
+/* ---- dropout on the LoRA branch ----------------------------------------------
+ * (deep dive, section 12: LoraConfig's lora_dropout = 0.05.)  In training the branch
+ * takes drop(x) for x and the base x itself:
+ *   y = x W_hat + s (drop(x) A) B,      drop(v)[m, k] = mask[m, k] v[m, k] / (1 - p),
+ * and by the chain rule, with u = s dy B^T as before,
+ *   dx = dy W_hat^T + drop(u A^T),   dA = drop(x)^T u,   dB = t^T dy,   t = s drop(x) A.
+ * The mask is never stored: each call makes it again from (seed, offset), so the
+ * backward is given what the forward was given.  It comes from the counter-based
+ * generator Philox-4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011): with key = seed (low word first) and counter =
+ * (k / 8, m, low word of offset, high word of offset), the four words give the 8 columns
+ * 8 (k / 8) .. + 7 of row m 16 bits each, the low half of a word first; mask[m, k] = 1
+ * where these 16 bits are at least P = round(65536 p) (ties to even), and 1 - p above
+ * stands for 1 - P / 65536.  Layers and steps that must not share a mask take other
+ * offsets or seeds; a mask depends on neither M, N, K nor r.
+ * A dropped value counts as zero, whatever it is.  The factor 1 / (1 - p) is applied to
+ * fp32 sums: no 16-bit value is rounded for it.
+ * 0 <= p < 1 and P <= 65535, otherwise INVALID_ARG; P = 0 is the call without dropout,
+ * bit for bit.  bf16 and fp16 only. */
+typedef struct qlora_dropout {
+    uint64_t seed;
+    uint64_t offset;
+    double p;
+} qlora_dropout;
+
+/* qlora_lora_down_batch with dropout: out_i = s drop_i(x_i) A_i, the t of a layer's
+ * forward (then qlora_fused_gemm_fwd, qlora_int8_gemm_fwd).  drops: an array of count, one for each
+ * item.  Workspace and errors as qlora_lora_down_batch; drops NULL -> INVALID_ARG. */
+qlora_status qlora_lora_down_batch_dropout(const qlora_lora_prod* items, const qlora_dropout* drops, int count, int r,
+                                           float alpha, int dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* qlora_lora_grads_batch with dropout: dA = drop_i(x)^T u, dB = t^T dy.  drops: an array of
+ * count.  Workspace and errors as qlora_lora_grads_batch; drops NULL -> INVALID_ARG. */
+qlora_status qlora_lora_grads_batch_dropout(const qlora_lora_grads* layers, const qlora_dropout* drops, int count,
+                                            int r, int dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* The input gradient with dropout, dx = dy W_hat^T + drop(u A^T): the calls without it
+ * plus drop (NULL -> INVALID_ARG), with their workspaces and errors.  (N, K) as there. */
+qlora_status qlora_linear_bwd_dx_dropout(const qlora_nf4* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                         float alpha, const qlora_dropout* drop, const uint16_t* dy, uint16_t* u,
+                                         uint16_t* dx, void* ws, size_t ws_bytes, void* stream);
+qlora_status qlora_fused_gemm_bwd_dx_dropout(const qlora_nf4* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                             const uint16_t* A, int r, const qlora_dropout* drop, uint16_t* dx,
+                                             void* stream);
+qlora_status qlora_int8_linear_bwd_dx_dropout(const qlora_int8* w, int64_t M, const uint16_t* A, const uint16_t* B,
+                                              int r, float alpha, const qlora_dropout* drop, const uint16_t* dy,
+                                              uint16_t* u, uint16_t* dx, void* ws, size_t ws_bytes, void* stream);
+qlora_status qlora_int8_gemm_bwd_dx_dropout(const qlora_int8* w, const uint16_t* dy, int64_t M, const uint16_t* u,
+                                            const uint16_t* A, int r, const qlora_dropout* drop, uint16_t* dx,
+                                            void* stream);
+
+/* ---- fp8: an 8-bit floating-point frozen base ---------------------------------
+ * (deep dive, sections 8.1 - 8.3: a low-bit storage format of its own, apart from the
+ * compute dtype.)  A tensor [rows, cols] is held as e4m3 codes (OCP: 4 exponent bits with
+ * bias 7, 3 mantissa bits, largest value 448, no infinity) with a power-of-two scale for
+ * each block, a byte e that stands for 2^(e - 127) (E8M0).  A weight W [N, K] has blocks of
+ * 128 x 128, activations and gradients blocks of 128 along a row; the last blocks may be
+ * short.  With a = max |x| over a block,
+ *   e = the least integer, 0 or more, with a <= 448 * 2^(e - 127),
+ *   code = x / 2^(e - 127) rounded to e4m3, ties to even;   a = 0: e = 0 and codes 0.
+ * A code stands for code * 2^(e - 127); rounding may bring the type's largest values up to the
+ * next power of two, which counts as such in products and is an infinity in 16 bits.  With powers of two the codes lose nothing to the
+ * scale's own rounding, and the matrix unit applies them by itself.  Inputs need not be
+ * finite: a block that holds an infinity or a NaN gets e = 255 (NaN) and codes 0, and every
+ * output that it takes part in is NaN.
+ * Scale bytes lie as [ceil(rows / 128)][S], S = ceil(cols / 128) rounded up to a multiple of
+ * 4, for block_rows = 128, and as [ceil(cols / 128)][S], S = rows rounded up to a multiple
+ * of 4, for block_rows = 1 (neighbouring rows side by side); the bytes that pad S are 0. */
+typedef struct qlora_fp8 {
+    uint8_t* codes;     /* [rows, cols] row-major                                   */
+    uint8_t* scale;     /* see above                                                */
+    int64_t rows;       /* N of a weight, M of activations                          */
+    int64_t cols;       /* K, a multiple of 64                                      */
+    int32_t dtype;      /* a qlora_dtype, bf16 or fp16: the 16-bit format of the    */
+                        /* tensors it is used with; any other -> INVALID_ARG        */
+    int32_t block_rows; /* 128 (a weight) or 1; any other -> INVALID_ARG            */
+} qlora_fp8;
+
+/* Bytes of the scales of a [rows, cols] tensor (0 for rows < 0, cols < 1 or another
+ * block_rows). */
+size_t qlora_fp8_scale_bytes(int64_t rows, int64_t cols, int block_rows);
+
+/* Quantize x [rows, cols] (bf16 or fp16 by out->dtype) into out.  rows == 0 is a no-op.
+ * Errors: null pointer, rows < 0, cols < 1, another dtype or block_rows -> INVALID_ARG;
+ * cols % 64, cols of 2^22 or more or rows above 2^31 - 16384 -> UNSUPPORTED_SHAPE;
+ * alignment -> MISALIGNED (codes, scale and x 16 bytes). */
+qlora_status qlora_fp8_quantize(const uint16_t* x, const qlora_fp8* out, void* stream);
+
+/* The values that the codes stand for, rounded to the 16-bit dtype, into out [rows, cols].
+ * Errors as qlora_fp8_quantize. */
+qlora_status qlora_fp8_dequantize(const qlora_fp8* q, uint16_t* out, void* stream);
+
+/* Forward of the fp8 linear layer with its LoRA branch (w->block_rows == 128):
+ *   xq = the 8-bit x, in blocks of 128 along its rows
+ *   t = s * (drop(x) A)                                [M, r], s = alpha / r
+ *   y[m, n] = RNE_16( sum_k xq[m,k] wq[n,k] + sum_j t[m,j] B[j,n] )
+ * t is rounded to 16 bits, also where the caller keeps none.  drop NULL: x itself.  r == 0:
+ * no LoRA branch (A, B, drop and t_out NULL; alpha is not used), 1 <= r <= 128 otherwise;
+ * t_out is nullable.  qlora_fp8_gemm_fwd is the product for a given xq (block_rows == 1)
+ * and t (t, B NULL when r == 0); it may add y's fp32 sums in another order (the last bit
+ * may differ).  Sums are fp32, except that the matrix unit adds 8 products of codes at a
+ * time and cuts off what lies 13 or more bits below the largest of them.
+ * M == 0 is a no-op.  Errors as qlora_linear_fwd, plus N or K of 2^22 or more, or M above
+ * 2^31 - 16384 -> UNSUPPORTED_SHAPE. */
+size_t qlora_fp8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r);
+qlora_status qlora_fp8_linear_fwd(const qlora_fp8* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                                  const uint16_t* B, int r, float alpha, const qlora_dropout* drop, uint16_t* y,
+                                  uint16_t* t_out, void* ws, size_t ws_bytes, void* stream);
+qlora_status qlora_fp8_gemm_fwd(const qlora_fp8* w, const qlora_fp8* x, const uint16_t* t, const uint16_t* B, int r,
+                                uint16_t* y, void* stream);
+
+/* Input gradient of the fp8 layer (the base is frozen: no dW):
+ *   dyq = the 8-bit dy, in blocks of 128 along its rows (N may be any size)
+ *   u  = s * (dy B^T)            [M, r]  into the caller's u (kept for qlora_lora_grads_batch)
+ *   dx[m, k] = RNE_16( sum_n dyq[m,n] wq[n,k] + drop( sum_j u[m,j] A[k,j] ) )
+ * from the one stored weight.  drop NULL: nothing is dropped.  r == 0: A, B, drop and u NULL.
+ * M == 0 is a no-op.  Errors as qlora_fp8_linear_fwd. */
+size_t qlora_fp8_linear_bwd_dx_workspace(int64_t M, int64_t N, int64_t K, int r);
+qlora_status qlora_fp8_linear_bwd_dx(const qlora_fp8* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                     float alpha, const qlora_dropout* drop, const uint16_t* dy, uint16_t* u,
+                                     uint16_t* dx, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
