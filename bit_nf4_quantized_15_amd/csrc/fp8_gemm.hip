@@ -104,6 +104,20 @@ __device__ __forceinline__ void tile_of(const TileMap& tp, int bid, int& mt, int
     mt = g * tp.gm + in - nt * rows;
 }
 
+// Schedule of a depth: its LDS reads spread over the first 1 / PARTS of its MFMAs, its direct loads
+// over all of them, so that the matrix unit is fed from the start and the reads are done early.
+template <int READS, int LOADS, int MFMAS, int PARTS>
+__device__ __forceinline__ void pace() {
+    constexpr int kFront = MFMAS / PARTS > 0 ? MFMAS / PARTS : 1;
+    constexpr int kR = (READS + kFront - 1) / kFront, kD = (LOADS + MFMAS - 1) / MFMAS;
+#pragma unroll
+    for (int m = 0; m < MFMAS; ++m) {
+        if (m < kFront) __builtin_amdgcn_sched_group_barrier(0x100, kR, 0);
+        if (LOADS) __builtin_amdgcn_sched_group_barrier(0x010, kD, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+}
+
 enum Branch { kPlain = 0, kLora = 1, kLoraDrop = 2 };
 
 // NWM x NWN waves, each MT x NT MFMA tiles of 32 tokens x 32 outputs; RING steps' tiles in LDS.
@@ -237,15 +251,20 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
             q.x[i] = join(*reinterpret_cast<const u32x4_t*>(p + offX[kk][0]), *reinterpret_cast<const u32x4_t*>(p + offX[kk][1]));
         }
     };
+    // (a wave's outputs are in one block of 128 where its width divides 128 and the tile's start is a block's)
+    constexpr int kWS = 128 % (32 * NT) == 0 && kBN % 128 == 0 ? 1 : NT;
     auto read_scales = [&](const uint8_t* __restrict__ slot, int ks, Scales& q) __attribute__((always_inline)) {
         const uint8_t* p = slot + kXB + kWB + 512 * wave;
 #pragma unroll
         for (int i = 0; i < MT; ++i) q.x[i] = p[32 * (MT * wm + i) + l32];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < kWS; ++i) {   // the byte wanted is brought down to bits 7..0
             const int o = 32 * (NT * wn + i);
-            q.w[i] = p[256 + o + (DX ? ((n0 + o) >> 7) & 3 : (first + ks) & 3)];
+            q.w[i] = (int)(*reinterpret_cast<const uint32_t*>(p + 256 + o) >>
+                           (8 * (DX ? ((n0 + o) >> 7) & 3 : (first + ks) & 3)));
         }
+#pragma unroll
+        for (int i = kWS; i < NT; ++i) q.w[i] = q.w[0];
     };
     f32x16_t acc[MT][NT];
     auto multiply = [&](const Ops& q, const Scales& s) __attribute__((always_inline)) {
@@ -257,6 +276,16 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
                     __builtin_bit_cast(i32x8_t, q.w[j]), __builtin_bit_cast(i32x8_t, q.x[i]), acc[i][j], 0, 0, 0, s.w[j], 0,
                     s.x[i]);
     };
+
+    // The products of a depth stay in front of the barrier that follows (nothing else orders them: the
+    // compiler moved a whole depth's behind it, 1.2 us per step of 256 x 256 where 0.9 are needed).
+    auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    constexpr int kReads = 2 * MT + (DX ? 4 : 2) * NT;   // LDS reads of a depth
 
     // ---- the LoRA term's operands.  t or u as MFMA operands: a lane holds ranks 16 kk + 8 h .. of its token
     const rsrc_t trs = buf_rsrc(LORA ? g.t + (int64_t)m0 * r : nullptr, (uint64_t)min(M - m0, kBM) * r * 2);
@@ -287,6 +316,15 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
         return n0 + row < O && j < r ? load8(g.L + (int64_t)(n0 + row) * r + j, r - j) : u32x4_t{0u, 0u, 0u, 0u};
     };
 
+    // chunk tid + kThreads e of rows of 64 ranks, 8 chunks a row
+    auto load_row = [&](rsrc_t rs, const uint16_t* p, int rows, int e) __attribute__((always_inline)) {
+        const int c = tid + kThreads * e, row = c >> 3, j = 8 * (c & 7);
+        if (VEC)
+            return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   rs, j < r ? (uint32_t)(row * r + j) * 2u : kNone, 0, 0));
+        return row < rows && j < r ? load8(p + (int64_t)row * r + j, r - j) : u32x4_t{0u, 0u, 0u, 0u};
+    };
+
     // ---- main loop
     uint8_t* const slots[4] = {s0, s1, s2, s3};
 #pragma unroll
@@ -300,7 +338,8 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const u32x4_t z = {0u, 0u, 0u, 0u};
+            u32x4_t z = {0u, 0u, 0u, 0u};
+            asm volatile("" : "+v"(z));   // (an operand of its own, or the products become one and its copies)
             acc[i][j] = mfma16<DT>(z, z, f32x16_t{});
         }
     if constexpr (RING == 2) {
@@ -315,6 +354,8 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
         auto step = [&](int ks, uint8_t* cur, const uint8_t* next) __attribute__((always_inline)) {
             read(cur, 1, b);
             multiply(a, sa);
+            pin();
+            pace<kReads, 0, MT * NT, 2>();
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
@@ -324,6 +365,8 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
             read_scales(next, ks + 1, sb);
             multiply(b, sa);
             sa = sb;
+            pin();
+            pace<kReads + MT + kWS, kLoads, MT * NT, 2>();
             __builtin_amdgcn_sched_barrier(0);
         };
         for (int ks = 0; ks < NS; ks += 2) {   // whole turns: steps past the end multiply zeros
@@ -346,10 +389,14 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
             read(next, 0, an);
             read_scales(next, ks + 1, sn);
             multiply(a, sa);
+            pin();
+            pace<kReads + MT + kWS, kXL + 1, MT * NT, 1>();
             __builtin_amdgcn_sched_barrier(0);
             load_w(fill, ks + 3);
             read(next, 1, bn);
             multiply(b, sa);
+            pin();
+            pace<kReads, kWL + 1, MT * NT, 1>();
             a = an;
             b = bn;
             sa = sn;
@@ -429,16 +476,46 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
     uint8_t* const e1 = RING == 2 ? s0 + kPart : s1;
     uint8_t* const e2 = RING == 2 ? s1 : s2;
     uint8_t* const e3 = RING == 2 ? s1 + kPart : s3;
-    if constexpr (LORA && !DX) {
-        auto put_b = [&](uint8_t* slot, int e, u32x4_t v) __attribute__((always_inline)) {
-            const int c = tid + kThreads * e, row = c / kCh, cc = c % kCh;
-            *reinterpret_cast<u32x4_t*>(slot + row * kRow + 16 * (cc ^ ((row & 3) << 1))) = v;
+    // t (or u) of up to 64 ranks goes to e2 in rows of 128 bytes, and A's rows to e1 the same way:
+    // all of it requested at once.  (Ranks 64 on are read from memory as operands.)
+    const bool staged = LORA && r <= 64;
+    if constexpr (LORA) {
+        constexpr int kTPer = kBM * 8 / kThreads, kAPer = kBN * 8 / kThreads;
+        static_assert(kBM * 128 <= kPart && kBN * 128 <= kPart, "operands of 64 ranks fit their parts");
+        auto put = [&](uint8_t* slot, int e, u32x4_t v) __attribute__((always_inline)) {
+            const int c = tid + kThreads * e;
+            *reinterpret_cast<u32x4_t*>(slot + tile_byte(c >> 3, c & 7)) = v;
         };
+        u32x4_t tv[kTPer], lv[DX ? kAPer : kBPer];
+        if (staged)
 #pragma unroll
-        for (int e = 0; e < kBPer; ++e) put_b(e1, e, load_b(0, e));
-        if (r > 64)
+            for (int e = 0; e < kTPer; ++e) tv[e] = load_row(trs, g.t + (int64_t)m0 * r, min(M - m0, kBM), e);
+        if constexpr (DX) {
+            if (staged)
 #pragma unroll
-            for (int e = 0; e < kBPer; ++e) put_b(e2, e, load_b(64, e));
+                for (int e = 0; e < kAPer; ++e) lv[e] = load_row(ars, g.L + (int64_t)n0 * r, min(O - n0, kBN), e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kBPer; ++e) lv[e] = load_b(0, e);
+        }
+        if (staged)
+#pragma unroll
+            for (int e = 0; e < kTPer; ++e) put(e2, e, tv[e]);
+        if constexpr (DX) {
+            if (staged)
+#pragma unroll
+                for (int e = 0; e < kAPer; ++e) put(e1, e, lv[e]);
+        } else {
+            auto put_b = [&](uint8_t* slot, int e, u32x4_t v) __attribute__((always_inline)) {
+                const int c = tid + kThreads * e, row = c / kCh, cc = c % kCh;
+                *reinterpret_cast<u32x4_t*>(slot + row * kRow + 16 * (cc ^ ((row & 3) << 1))) = v;
+            };
+#pragma unroll
+            for (int e = 0; e < kBPer; ++e) put_b(e1, e, lv[e]);
+            if (r > 64)
+#pragma unroll
+                for (int e = 0; e < kBPer; ++e) put_b(e2, e, load_b(64, e));
+        }
         __syncthreads();
     }
     const int tj = l32 & 15, tg = l32 >> 4;
@@ -453,13 +530,15 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
 #pragma unroll
         for (int j = 0; j < NT; ++j) f[j] = LORA == kLoraDrop ? f32x16_t{} : acc[i][j];
         if constexpr (LORA) {
-            for (int kk = 0; 16 * kk < r; ++kk) {
-                const u32x4_t a = load_t(i, kk);
+            auto rank16 = [&](int kk, bool lds) __attribute__((always_inline)) {
+                const u32x4_t a = lds ? *reinterpret_cast<const u32x4_t*>(e2 + tile_byte(32 * (MT * wm + i) + l32, 2 * kk + h))
+                                      : load_t(i, kk);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     u32x4_t b;
                     if constexpr (DX) {
-                        b = load_a(j, kk);
+                        b = lds ? *reinterpret_cast<const u32x4_t*>(e1 + tile_byte(32 * (NT * wn + j) + l32, 2 * kk + h))
+                                : load_a(j, kk);
                     } else {   // rows 16 kk + 8 h .. + 7 of B, column l32 of each tile, by two transposed reads
                         const uint8_t* slot = kk < 4 ? e1 : e2;
                         const int row = 16 * (kk & 3) + 8 * h + (tj >> 2), col = 32 * (NT * wn + j) + 16 * tg + 4 * (tj & 3);
@@ -470,7 +549,11 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
                     }
                     f[j] = mfma16<DT>(b, a, f[j]);
                 }
-            }
+            };
+            if (staged)
+                for (int kk = 0; 16 * kk < r; ++kk) rank16(kk, true);
+            else
+                for (int kk = 0; 16 * kk < r; ++kk) rank16(kk, false);
         }
         if constexpr (LORA == kLoraDrop) {
 #pragma unroll
@@ -478,6 +561,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, MT* NT >= 4 ? 1 : 2) void fp8_gemm_
                 drop_tile(f[j], g.drop, (uint32_t)(m0 + 32 * (MT * wm + i) + l32), (uint32_t)(n0 + 32 * (NT * wn + j)), h);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) f[j][v] += acc[i][j][v];
+                __builtin_amdgcn_sched_barrier(0);   // (a tile at a time, or their temporaries spill)
             }
         }
         // lane (h, l32): token l32 of the 32, outputs 32 j + 8 v4 + 4 h + 0..3
