@@ -53,4 +53,12 @@ struct Fp8Gemm {
 size_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, bool dx);
 qlora_status launch_fp8_gemm(const Fp8Gemm& g, bool dx, int dt, void* ws, hipStream_t s);
 
+// The forward for up to kFp8GemvMaxM tokens in one launch (fp8_gemv_supported).  x 16-bit, quantized
+// by the kernel (g.x null; fp8_gemv_quantizes says for which sizes), or its codes; t given (g.t),
+// or made from x (then not null) and A in the launch, t = RNE_16(scale x A), with
+// fp8_gemv_workspace(r) bytes of workspace that need no clearing, and stored to t_out (nullable).
+size_t fp8_gemv_workspace(int r);
+qlora_status launch_fp8_gemv(const Fp8Gemm& g, const uint16_t* x, const uint16_t* A, float scale, uint16_t* t_out,
+                             void* ws, int dt, hipStream_t s);
+
 }  // namespace qlora

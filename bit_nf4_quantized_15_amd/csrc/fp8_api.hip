@@ -64,7 +64,7 @@ Ws layer_ws(int64_t M, int64_t N, int64_t K, int r, bool dx) {
     w.tbuf = w.scale + align256((size_t)fp8_blocks(C) * w.rs);
     w.prep = w.tbuf + (dx ? 0 : align256((size_t)M * r * 2));
     w.part = w.prep + (r ? align256(fp8_prep_ws(M, C, r)) : 0);
-    w.total = w.part + fp8_gemm_workspace(M, N, K, dx);
+    w.total = w.part + (!dx && fp8_gemv_supported(M, K) ? fp8_gemv_workspace(r) : fp8_gemm_workspace(M, N, K, dx));
     return w;
 }
 
@@ -126,11 +126,19 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8* w, const uint16_t* x, int64_t
     const int dt = dt_of(w->dtype);
     uint8_t *xq = at(ws, 0), *sx = at(ws, W.scale);
     uint16_t* t = t_out ? t_out : reinterpret_cast<uint16_t*>(at(ws, W.tbuf));
+    Fp8Gemm g{xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, (int)W.ld, W.rs,
+              scale_stride(N, K, kFp8Block), DropArgs{}};
+    const bool few = fp8_gemv_supported(M, K);
+    if (few && !d.thr) {   // t and, where there is room, the codes of x in the launch itself
+        if (fp8_gemv_quantizes(M, K)) g.x = nullptr;
+        else if ((st = launch_fp8_quantize_rows(x, M, K, xq, W.ld, sx, W.rs, dt, s)) != QLORA_OK) return st;
+        g.t = nullptr;
+        return launch_fp8_gemv(g, x, A, r ? alpha / (float)r : 0.0f, t_out, at(ws, W.part), dt, s);
+    }
     st = r ? launch_fp8_prep(x, A, true, d, alpha / (float)r, (int)M, (int)K, r, xq, W.ld, sx, W.rs, t, at(ws, W.prep), dt, s)
            : launch_fp8_quantize_rows(x, M, K, xq, W.ld, sx, W.rs, dt, s);
     if (st != QLORA_OK) return st;
-    const Fp8Gemm g{xq, sx, w->codes, w->scale, r ? t : nullptr, B, y, (int)M, (int)N, (int)K, r, (int)W.ld, W.rs,
-                    scale_stride(N, K, kFp8Block), DropArgs{}};
+    if (few) return launch_fp8_gemv(g, nullptr, nullptr, 0.0f, nullptr, nullptr, dt, s);
     return launch_fp8_gemm(g, false, dt, at(ws, W.part), s);
 }
 
@@ -144,6 +152,8 @@ qlora_status qlora_fp8_gemm_fwd(const qlora_fp8* w, const qlora_fp8* x, const ui
     if (!aligned16(y) || !aligned16(t) || !aligned16(B)) return QLORA_ERR_MISALIGNED;
     const Fp8Gemm g{x->codes, x->scale, w->codes, w->scale, t, B, y, (int)x->rows, (int)w->rows, (int)w->cols, r,
                     (int)x->cols, pad4(x->rows), scale_stride(w->rows, w->cols, kFp8Block), DropArgs{}};
+    if (fp8_gemv_supported(g.M, g.K))
+        return launch_fp8_gemv(g, nullptr, nullptr, 0.0f, nullptr, nullptr, dt_of(w->dtype), (hipStream_t)stream);
     return launch_fp8_gemm(g, false, dt_of(w->dtype), nullptr, (hipStream_t)stream);
 }
 

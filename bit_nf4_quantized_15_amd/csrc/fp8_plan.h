@@ -21,6 +21,13 @@ inline SplitPlan plan_fp8_prep(int64_t M, int64_t C, int r) {
     return sp;
 }
 
+// ---- forward, up to kFp8GemvMaxM tokens: one launch
+constexpr int kFp8GemvMaxM = 16;
+// (LDS holds the scales of 16 tokens: K / 8 bytes)
+inline bool fp8_gemv_supported(int64_t M, int64_t K) { return M <= kFp8GemvMaxM && K <= (int64_t(1) << 18); }
+// (the codes of x beside the rest in LDS, rows of whole runs of 512 and 16 bytes)
+inline bool fp8_gemv_quantizes(int64_t M, int64_t K) { return M * ((K + 511) / 512 * 512 + 16) <= (int64_t(72) << 10); }
+
 // ---- products
 enum Fp8Tile { kFp8T256x256, kFp8T128x128, kFp8T64x64 };
 struct Fp8Choice {
