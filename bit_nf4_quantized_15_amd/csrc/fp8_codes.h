@@ -18,6 +18,16 @@ __device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
                                                                   __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu)));
 }
 
+// The largest 16-bit pattern in m's halves over the 16 lanes of a DPP row (rotations within the
+// row: a VALU instruction each, where a shuffle goes through LDS).
+__device__ __forceinline__ uint32_t max_row16(uint32_t m) {
+    uint32_t t = max(m & 0xFFFFu, m >> 16);
+    t = max(t, (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0x128, 0xF, 0xF, true));
+    t = max(t, (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0x124, 0xF, 0xF, true));
+    t = max(t, (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0x122, 0xF, 0xF, true));
+    return max(t, (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0x121, 0xF, 0xF, true));
+}
+
 // Scale byte of a block whose largest magnitude has the 16-bit pattern a: the least e >= 0 with
 // value <= 448 2^(e - 127).  448 = 1.75 * 2^8, so e is the exponent field less 8, one more where
 // the fraction is above 0.75; what is subnormal in fp32 is far below 448 * 2^-127.

@@ -13,14 +13,6 @@
 namespace qlora {
 namespace {
 
-// Largest magnitude (16-bit pattern) of a packed pair's halves over the 16 lanes of a block.
-__device__ __forceinline__ uint32_t max16(uint32_t m) {
-    uint32_t t = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-    for (int d = 8; d; d >>= 1) t = max(t, (uint32_t)__shfl_xor((int)t, d));
-    return t;
-}
-
 // 8 values of a row at column c of `cols`, zero past them.
 template <bool VEC>
 __device__ __forceinline__ u32x4_t load8(const uint16_t* __restrict__ row, int64_t c, int64_t cols, bool on) {
@@ -54,7 +46,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restric
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max_mag2(m, v[b][i]);
-        const uint32_t byte = fp8_scale_byte<DT>(max16(m));
+        const uint32_t byte = fp8_scale_byte<DT>(max_row16(m));
         const int64_t c = c0 + b * kFp8Block;
         if (on && c < ld) *reinterpret_cast<u32x2_t*>(codes + row * ld + c) = fp8_codes8<DT>(v[b], byte);
         const int64_t block = bx * kBlocksWg + b;
@@ -78,7 +70,7 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(const uint16_t* __restr
     for (int p = 0; p < 8; ++p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max_mag2(m, v[p][i]);
-    m = max16(m);
+    m = max_row16(m);
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     if ((threadIdx.x & 63) == 0) am[threadIdx.x >> 6] = m;
