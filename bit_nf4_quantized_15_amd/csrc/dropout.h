@@ -32,9 +32,9 @@ __device__ __forceinline__ u32x4_t drop_words(const DropArgs& d, uint32_t group,
 #pragma unroll
     for (int i = 0; i < kPhiloxRounds; ++i) {
         const uint64_t a = (uint64_t)c0 * kPhiloxM0, b = (uint64_t)c2 * kPhiloxM1;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(b >> 32), c1, k0, 0x96);   // (xor of three)
         c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(a >> 32), c3, k1, 0x96);
         c3 = (uint32_t)a;
         k0 += kPhiloxW0;
         k1 += kPhiloxW1;
@@ -42,20 +42,20 @@ __device__ __forceinline__ u32x4_t drop_words(const DropArgs& d, uint32_t group,
     return u32x4_t{c0, c1, c2, c3};
 }
 
-// All ones in the halves of w that are kept.  thr > 0.
-__device__ __forceinline__ uint32_t keep_halves(uint32_t w, uint32_t thr) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    const u16x2 t = {(uint16_t)(thr - 1u), (uint16_t)(thr - 1u)}, one = {1, 1};
-    const u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w), t);   // 0 where w < thr
-    const u16x2 k = __builtin_elementwise_min(over, one);
-    return __builtin_bit_cast(uint32_t, (u16x2)(u16x2{0, 0} - k));
+// All ones in the halves of w that are dropped: the sign of (w - 2^15) - (thr - 2^15), subtracted
+// with saturation as signed 16-bit numbers.
+__device__ __forceinline__ uint32_t dropped_halves(uint32_t w, uint32_t thr) {
+    typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t t = (thr | (thr << 16)) ^ 0x80008000u;
+    const i16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(i16x2, w ^ 0x80008000u), __builtin_bit_cast(i16x2, t));
+    return __builtin_bit_cast(uint32_t, (i16x2)(d >> (int16_t)15));
 }
 
 // 8 consecutive 16-bit values of row m with the dropped ones zero.
 __device__ __forceinline__ u32x4_t drop8(u32x4_t v, const DropArgs& d, uint32_t group, uint32_t m) {
     const u32x4_t w = drop_words(d, group, m);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] &= keep_halves(w[i], d.thr);
+    for (int i = 0; i < 4; ++i) v[i] &= ~dropped_halves(w[i], d.thr);
     return v;
 }
 

@@ -13,14 +13,6 @@ constexpr int kFp8Block = 128;
 inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
-// ---- preparation (codes and t, or u, in one pass): plan_nt in whole blocks of 128
-inline SplitPlan plan_fp8_prep(int64_t M, int64_t C, int r) {
-    SplitPlan sp = plan_nt(M, C, r);
-    sp.chunk = (sp.chunk + kFp8Block - 1) / kFp8Block * kFp8Block;
-    sp.splits = (int)((C + sp.chunk - 1) / sp.chunk);
-    return sp;
-}
-
 // ---- forward, up to kFp8GemvMaxM tokens: one launch
 constexpr int kFp8GemvMaxM = 16;
 // (LDS holds the scales of 16 tokens: K / 8 bytes)

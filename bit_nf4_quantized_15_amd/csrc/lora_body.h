@@ -1,10 +1,9 @@
-// Bodies of the LoRA side-path kernels, shared by the kernels without dropout (lora.hip),
-// those with it (lora_dropout.hip) and those that also make 8-bit codes (fp8_prep.hip).
+// Bodies of the LoRA side-path kernels, shared by the kernels without dropout (lora.hip) and
+// those with it (lora_dropout.hip).
 #pragma once
 
 #include "common.h"
 #include "dropout.h"
-#include "fp8_codes.h"
 #include "lora_plan.h"
 #include "split_sync.h"
 
@@ -161,50 +160,11 @@ __device__ __forceinline__ bool split_sum(f32x16_t (&acc)[TQ], uint64_t* __restr
 // columns c + 32h .. c + 32h + 31 of each 64-column step (the two halves of an
 // MFMA's k slots may map to any reduction indices, as long as both operands
 // agree).
-// DROP: drop(X) instead of X (more.drop.thr may be 0: then X).  QUANT: the same pass
-// writes X in 8 bits, rows in blocks of 128 (fp8.h); splits and NST are whole blocks, a
-// block's 128 columns are two steps of the lanes l and l + 32.
-struct NtMore {
-    DropArgs drop;
-    uint8_t* codes;   // [M][ld]
-    uint8_t* scale;   // [ceil(C / 128)][rs]
-    int64_t ld, rs;
-};
-// One block of row xrow: a lane half h holds columns col + 32 h .. + 31 (a) and col + 64 + 32 h ..
-// + 31 (b).  Columns past the row's end are zero in a and b, and zero codes up to ld.
-template <int DT>
-__device__ __forceinline__ void nt_quantize(const bf16x8 (&a)[4], const bf16x8 (&b)[4], bool on, int col, int xrow,
-                                            int h, const NtMore& more) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const u32x4_t va = __builtin_bit_cast(u32x4_t, a[i]), vb = __builtin_bit_cast(u32x4_t, b[i]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = max_mag2(max_mag2(top, va[w]), vb[w]);
-    }
-    top = max(top & 0xFFFFu, top >> 16);
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-    const uint32_t byte = fp8_scale_byte<DT>(top);
-    if (!on) return;
-    if (h == 0) more.scale[(int64_t)(col >> 7) * more.rs + xrow] = (uint8_t)byte;
-    uint8_t* const row = more.codes + (int64_t)xrow * more.ld;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const int c = col + 64 * e + 32 * h + 8 * i;
-            const u32x2_t lo = fp8_codes8<DT>(__builtin_bit_cast(u32x4_t, e ? b[i] : a[i]), byte);
-            const u32x2_t hi = fp8_codes8<DT>(__builtin_bit_cast(u32x4_t, e ? b[i + 1] : a[i + 1]), byte);
-            if (c < more.ld) *reinterpret_cast<u32x4_t*>(row + c) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-        }
-}
-
-template <int TQ, bool VEC, bool YNAT, int NST, int DT, bool DROP = false, bool QUANT = false>
+template <int TQ, bool VEC, bool YNAT, int NST, int DT>
 __device__ __forceinline__ void nt_body(const uint16_t* __restrict__ X, const uint16_t* __restrict__ Y,
                                         uint64_t* __restrict__ tags, float* __restrict__ part,
                                         uint16_t* __restrict__ out, float scale, int M, int C, int r, int chunk,
-                                        int tile, int split, int tiles, int splits, const NtMore& more = NtMore{}) {
-    static_assert(!QUANT || NST % 2 == 0, "whole blocks");
+                                        int tile, int split, int tiles, int splits) {
     static_assert(NST * 64 <= (TQ == 4 ? 256 : 512), "steps beyond nt_max_chunk");
     constexpr int kCols = NST * 64;                   // columns of C per split (at most)
     constexpr int kLdT = kCols + 8;                   // Yt row (bf16): 16 rows start 4 banks apart
@@ -265,17 +225,7 @@ __device__ __forceinline__ void nt_body(const uint16_t* __restrict__ X, const ui
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[q][v] = 0.0f;
 #pragma unroll
-    for (int st = 0; st < NST; ++st) {
-        if constexpr (QUANT) {
-            if (st % 2 == 0) nt_quantize<DT>(xa[st], xa[st + 1], xrow < M && c_begin + 64 * st < c_end, c_begin + 64 * st, xrow, h, more);
-        }
-        if (DROP && more.drop.thr) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                xa[st][i] = __builtin_bit_cast(
-                    bf16x8, drop8(__builtin_bit_cast(u32x4_t, xa[st][i]), more.drop,
-                                  (uint32_t)(c_begin + 64 * st + 32 * h + 8 * i) >> 3, (uint32_t)xrow));
-        }
+    for (int st = 0; st < NST; ++st)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -285,7 +235,6 @@ __device__ __forceinline__ void nt_body(const uint16_t* __restrict__ X, const ui
                                        : *reinterpret_cast<const bf16x8*>(&ys[(32 * q + l32) * kLdT + c]);
                 acc[q] = mfma32<DT>(xa[st][i], yb, acc[q]);
             }
-    }
     if (!split_sum<TQ>(acc, tags, part, tiles, tile, split, splits)) return;
 #pragma unroll
     for (int q = 0; q < TQ; ++q) {

@@ -1,10 +1,11 @@
-// The LoRA products of a training step with dropout (dropout.h): t = s drop(x) A and dA =
-// drop(x)^T u beside dB = t^T dy, for several layers in one launch each.  The bodies are those of
-// lora_body.h; a lane holds 8 consecutive columns of a row of x, the unit of the generator, and
-// masks them in registers between the load and the MFMA operand (t) or the LDS tile (dA).
+// The LoRA products of a training step with dropout (dropout.h): t = s drop(x) A (lora_prep.h) and
+// dA = drop(x)^T u beside dB = t^T dy for several layers in one launch (lora_body.h).  A lane
+// holds 8 consecutive columns of a row of x, the unit of the generator, and masks them in
+// registers between the load and the MFMA operand (t) or the LDS tile (dA).
 #include <cmath>
+#include <vector>
 
-#include "lora_body.h"
+#include "lora_prep.h"
 
 namespace qlora {
 
@@ -25,21 +26,10 @@ bool drop_args(const qlora_dropout* d, DropArgs* out) {
 
 namespace {
 
-struct NtDropBatch {
-    NtBatch b;
-    DropArgs drop[kNtBatch];
-};
-
-template <int TQ, bool VEC, int NST, int DT>
-__global__ __launch_bounds__(256) void ntb_dropout_kernel(const NtDropBatch bt) {
-    const int b = blockIdx.x;
-    int i = 0;
-    while (i + 1 < bt.b.n && b >= bt.b.first[i + 1]) ++i;
-    const NtProb& p = bt.b.p[i];
-    const int c = b - bt.b.first[i];
-    const NtMore more{bt.drop[i], nullptr, nullptr, 0, 0};
-    nt_body<TQ, VEC, true, NST, DT, true>(p.X, p.Y, p.tags, p.part, p.out, p.scale, p.M, p.C, bt.b.r, p.chunk,
-                                          c % p.tiles, c / p.tiles, p.tiles, p.splits, more);
+// (two workgroups on a CU where the ranks' registers allow)
+template <int TQ, bool VEC, int DT>
+__global__ __launch_bounds__(256, TQ <= 2 ? 2 : 1) void down_stream_kernel(const StreamArgs a) {
+    stream_body<TQ, VEC, true, true, false, DT>(a);
 }
 
 template <int TQ, bool VEC, int NST, int DT>
@@ -63,44 +53,61 @@ struct TnDropLaunch {
 
 }  // namespace
 
-qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s) {
-    const int tq = (r + 31) / 32;
-    for (int i0 = 0; i0 < count; i0 += kNtBatch) {
-        NtDropBatch db{};
-        bool vec = false;
-        int chunk = 64;
-        unsigned total = 0;
-        const qlora_status st = nt_batch(d + i0, std::min(kNtBatch, count - i0), true, r, db.b, vec, chunk, total);
-        if (st != QLORA_OK) return st;
-        for (int i = 0; i < db.b.n; ++i) {
-            db.drop[i] = drop[i0 + i];
-            db.b.p[i].scale *= drop[i0 + i].inv;
-        }
-        const int nst = steps_template(chunk);
-#define QL_D(TQ, V, NST) \
-    hipLaunchKernelGGL((ntb_dropout_kernel<TQ, V, NST, DT>), dim3(total), dim3(256), 0, s, db);
-#define QL_D1(TQ, V)                       \
-    if (nst == 2) { QL_D(TQ, V, 2) }       \
-    else if (nst == 4) { QL_D(TQ, V, 4) }  \
-    else { QL_D(TQ, V, (TQ == 4 ? 4 : 8)) }
-#define QL_D2(TQ) \
-    if (vec) { QL_D1(TQ, true) } else { QL_D1(TQ, false) }
-        with_dt(dt, [&](auto dtc) {
-            constexpr int DT = decltype(dtc)::value;
-            switch (tq) {
-                case 1: QL_D2(1) break;
-                case 2: QL_D2(2) break;
-                case 3: QL_D2(3) break;
-                default: QL_D2(4) break;
-            }
-        });
-#undef QL_D2
-#undef QL_D1
-#undef QL_D
-        const qlora_status ls = launch_status();
-        if (ls != QLORA_OK) return ls;
+namespace {
+
+// n <= kStreamItems products
+qlora_status down_stream(const NtDesc* d, const DropArgs* drop, int n, int r, int dt, hipStream_t s) {
+    StreamArgs a{};
+    bool vec = r % 8 == 0;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        a.item[i] = stream_item(d[i].X, d[i].Y, d[i].out, d[i].ws, drop[i], d[i].scale, d[i].M, d[i].C,
+                                plan_down(d[i].M, d[i].C, r, n));
+        // vector path: 16-byte rows, and one workgroup's rows under 1 GiB of buffer offsets
+        vec = vec && d[i].C % 8 == 0 && (int64_t)d[i].C * 128 * 2 < (int64_t(1) << 30);
+        a.first[i] = (int)total;
+        total += (int64_t)a.item[i].tiles * a.item[i].splits;
+        if (total * 256 >= (int64_t(1) << 32)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     }
-    return QLORA_OK;
+    a.first[n] = (int)total;
+    a.n = n;
+    a.r = r;
+    with_dt(dt, [&](auto dtc) {
+        constexpr int DT = decltype(dtc)::value;
+#define QL_S(TQ)                                                                                                    \
+    if (vec) hipLaunchKernelGGL((down_stream_kernel<TQ, true, DT>), dim3((unsigned)total), dim3(256), 0, s, a);    \
+    else hipLaunchKernelGGL((down_stream_kernel<TQ, false, DT>), dim3((unsigned)total), dim3(256), 0, s, a);
+        switch ((r + 31) / 32) {
+            case 1: QL_S(1) break;
+            case 2: QL_S(2) break;
+            case 3: QL_S(3) break;
+            default: QL_S(4) break;
+        }
+#undef QL_S
+    });
+    const qlora_status st = launch_status();
+    return st == QLORA_OK ? launch_reduce(a, dt, s) : st;
+}
+
+}  // namespace
+
+qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s) {
+    std::vector<NtDesc> plain, rest;   // (nothing dropped: the product of the call without dropout, bit for bit)
+    std::vector<DropArgs> rest_drop;
+    for (int i = 0; i < count; ++i) {
+        if (!drop[i].thr) {
+            plain.push_back(d[i]);
+            continue;
+        }
+        rest.push_back(d[i]);
+        rest_drop.push_back(drop[i]);
+    }
+    qlora_status st = QLORA_OK;
+    if (!plain.empty()) st = launch_nt_batch(plain.data(), (int)plain.size(), true, r, dt, s);
+    for (size_t i = 0; i < rest.size() && st == QLORA_OK; i += kStreamItems)
+        st = down_stream(rest.data() + i, rest_drop.data() + i, (int)std::min<size_t>(kStreamItems, rest.size() - i), r, dt,
+                         s);
+    return st;
 }
 
 qlora_status launch_tn_batch_dropout(const TnDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s) {
