@@ -382,6 +382,8 @@ static qlora_status lora_prod_batch(const qlora_lora_prod* items, const DropArgs
         const qlora_lora_prod& e = items[i];
         if (bad_dims(e.M, 1, e.C, r)) return QLORA_ERR_INVALID_ARG;
         if (y_natural && e.C % kBlock) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        // (the kernel with dropout counts columns in 32 bits, up to some blocks past the last)
+        if (drop && drop[i].thr && e.C > INT32_MAX - 1024) return QLORA_ERR_UNSUPPORTED_SHAPE;
         if (e.M == 0) continue;
         if (!e.x || !e.w || !e.out) return QLORA_ERR_INVALID_ARG;
         if (!aligned16(e.x) || !aligned16(e.w) || !aligned16(e.out)) return QLORA_ERR_MISALIGNED;

@@ -630,7 +630,8 @@ def _lora_prod_batch(fn, name, items, alpha, natural, outs, ws, dropout=None):
 def lora_down_batch(items, alpha, t=None, ws=None, dropout=None):
     """t_i = (alpha/r) x_i A_i for items [(x_i, A_i)] in one launch per 8 (qlora_lora_down_batch); each t_i is
     that of lora_down.  t: optional list of outputs.  dropout: optional list of Dropouts (None entries drop nothing),
-    then t_i = (alpha/r) drop_i(x_i) A_i (qlora_lora_down_batch_dropout).  Returns the list of t_i."""
+    then t_i = (alpha/r) drop_i(x_i) A_i (qlora_lora_down_batch_dropout; the last bit may depend on how many of the
+    items drop something).  Returns the list of t_i."""
     if dropout is not None:
         return _lora_prod_batch(lib.qlora_lora_down_batch_dropout, "qlora_lora_down_batch_dropout", items, alpha, True, t,
                                 ws, dropout)

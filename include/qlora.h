@@ -491,8 +491,11 @@ typedef struct qlora_dropout {
 } qlora_dropout;
 
 /* qlora_lora_down_batch with dropout: out_i = s drop_i(x_i) A_i, the t of a layer's
- * forward (then qlora_fused_gemm_fwd, qlora_int8_gemm_fwd).  drops: an array of count, one for each
- * item.  Workspace and errors as qlora_lora_down_batch; drops NULL -> INVALID_ARG. */
+ * forward (then qlora_fused_gemm_fwd, qlora_int8_gemm_fwd).  drops: an array of
+ * count, one for each item.  The order of an item's fp32 sums depends on how many items of the
+ * call drop something: out's last bit may differ between a call of one and a call of several.
+ * Workspace and errors as qlora_lora_down_batch; drops NULL -> INVALID_ARG; C above 2^31 - 1025
+ * of an item that drops something -> UNSUPPORTED_SHAPE. */
 qlora_status qlora_lora_down_batch_dropout(const qlora_lora_prod* items, const qlora_dropout* drops, int count, int r,
                                            float alpha, int dtype, void* ws, size_t ws_bytes, void* stream);
 
@@ -526,8 +529,9 @@ qlora_status qlora_int8_gemm_bwd_dx_dropout(const qlora_int8* w, const uint16_t*
  *   e = the least integer, 0 or more, with a <= 448 * 2^(e - 127),
  *   code = x / 2^(e - 127) rounded to e4m3, ties to even;   a = 0: e = 0 and codes 0.
  * A code stands for code * 2^(e - 127); rounding may bring the type's largest values up to the
- * next power of two, which counts as such in products and is an infinity in 16 bits.  With powers of two the codes lose nothing to the
- * scale's own rounding, and the matrix unit applies them by itself.  Inputs need not be
+ * next power of two, which counts as such in products and is an infinity in 16 bits.  With
+ * powers of two the codes lose nothing to the scale's own rounding, and the matrix unit applies
+ * them by itself.  Inputs need not be
  * finite: a block that holds an infinity or a NaN gets e = 255 (NaN) and codes 0, and every
  * output that it takes part in is NaN.
  * Scale bytes lie as [ceil(rows / 128)][S], S = ceil(cols / 128) rounded up to a multiple of
@@ -549,8 +553,8 @@ size_t qlora_fp8_scale_bytes(int64_t rows, int64_t cols, int block_rows);
 
 /* Quantize x [rows, cols] (bf16 or fp16 by out->dtype) into out.  rows == 0 is a no-op.
  * Errors: null pointer, rows < 0, cols < 1, another dtype or block_rows -> INVALID_ARG;
- * cols % 64, cols of 2^22 or more or rows above 2^31 - 16384 -> UNSUPPORTED_SHAPE;
- * alignment -> MISALIGNED (codes, scale and x 16 bytes). */
+ * cols % 64, cols of 2^22 or more, rows above 2^31 - 16384 or 2^36 elements or more ->
+ * UNSUPPORTED_SHAPE; alignment -> MISALIGNED (codes, scale and x 16 bytes). */
 qlora_status qlora_fp8_quantize(const uint16_t* x, const qlora_fp8* out, void* stream);
 
 /* The values that the codes stand for, rounded to the 16-bit dtype, into out [rows, cols].

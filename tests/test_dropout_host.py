@@ -84,6 +84,9 @@ def test_batch_arguments(q):
         assert f(good, ws=None) == WORKSPACE and f(good, nb=16) == WORKSPACE and f(good, ws=FAKE + 8) == MISALIGNED
     assert down(D(0.1, 0.1), alpha=float("inf")) == INVALID
     assert down(D(0.1, 0.1), items=(q.LoraProd * 2)(*[q.LoraProd(FAKE, FAKE, FAKE, 4, 100)] * 2)) == SHAPE
+    for C in (2 ** 31 - 64, 2 ** 31 - 1024):       # columns that the kernel could not count in 32 bits
+        wide = (q.LoraProd * 2)(q.LoraProd(FAKE, FAKE, FAKE, 4, 128), q.LoraProd(FAKE, FAKE, FAKE, 4, C))
+        assert down(D(0.0, 0.1), items=wide) == SHAPE
 
 
 def test_the_class(q):

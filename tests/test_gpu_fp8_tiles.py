@@ -105,3 +105,47 @@ def test_codes_of_a_layer_are_those_of_the_quantizer(q):
     y2, _ = q.fp8_linear_fwd(L.w, L.x)
     assert torch.equal(q.fp8_gemm_fwd(L.w, xq), y2)
     assert torch.equal(q.fp8_gemm_fwd(L.w, xq, t, L.B), y)
+
+
+def test_split_products_in_graphs_that_share_a_workspace(q):
+    """Two layers whose products are split, a graph each, on one workspace, replayed in turn; and at once on two
+    streams with a workspace each."""
+    import torch
+    say("[fp8] split products: graphs on one workspace, two streams")
+    Ls = [Layer(q, "bf16", 71, 649, 1728, 5312, 64), Layer(q, "bf16", 72, 464, 5120, 2112, 24)]
+    size = max(max(q.lib.qlora_fp8_fwd_workspace(L.M, L.N, L.K, L.r), q.lib.qlora_fp8_linear_bwd_dx_workspace(L.M, L.N, L.K, L.r))
+               for L in Ls)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda:0")
+    drop = q.Dropout(0.1, SEED, OFFSET)
+
+    def call(L, ws):
+        y, t = q.fp8_linear_fwd(L.w, L.x, L.A, L.B, L.alpha, ws=ws, dropout=drop)
+        u, dx = q.fp8_linear_bwd_dx(L.w, L.A, L.B, L.alpha, L.dy, ws=ws, dropout=drop)
+        return y, t, u, dx
+    want = [call(L, ws) for L in Ls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for L in Ls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(L, ws))
+        graphs.append(g)
+    for rep in range(3):
+        for i, g in enumerate(graphs):
+            for v in outs[i]:
+                v.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i])), (rep, i)
+        call(Ls[rep % 2], ws)
+        torch.cuda.synchronize()
+    streams, spaces = [torch.cuda.Stream() for _ in Ls], [ws, torch.empty_like(ws)]
+    got = [[], []]
+    for _ in range(3):
+        for i, L in enumerate(Ls):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call(L, spaces[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
