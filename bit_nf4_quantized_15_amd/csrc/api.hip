@@ -8,6 +8,7 @@
 
 #include "common.h"
 #include "dropout.h"
+#include "grads_plan.h"
 #include "lora_plan.h"
 
 using namespace qlora;
@@ -466,13 +467,14 @@ static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const DropA
         if (g.M == 0) continue;
         if (!g.x || !g.t || !g.u || !g.dy) return QLORA_ERR_INVALID_ARG;
         if (!aligned16(g.x) || !aligned16(g.t) || !aligned16(g.u) || !aligned16(g.dy)) return QLORA_ERR_MISALIGNED;
+        if (drop && drop[i].thr && (g.N >= kGradMaxWidth || g.K >= kGradMaxWidth)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     }
     const size_t need = qlora_lora_grads_batch_workspace(layers, count, r);
     if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
-    std::vector<TnDesc> d;
-    std::vector<DropArgs> dd;
+    std::vector<TnDesc> d;            // (layers that drop nothing: the call without dropout, bit for bit)
+    std::vector<GradDropDesc> dd;
     d.reserve(2 * (size_t)count);
     size_t off = 0;
     qlora_status st = QLORA_OK;
@@ -484,16 +486,15 @@ static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const DropA
             continue;
         }
         // dA [K, r] = x^T u ; dB [r, N] = t^T dy, stored transposed from the [N, r] reduction
-        if (drop) {   // (of x; nothing is dropped of dy)
-            dd.push_back(drop[i]);
-            dd.push_back(DropArgs{0u, 0u, 0u, 0u, 0u, 1.0f});
-        }
-        d.push_back(TnDesc{g.x, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1});
+        const bool drops = drop && drop[i].thr;
+        if (drops) dd.push_back(GradDropDesc{g.x, g.u, at(ws, off), g.dA, drop[i], (int)g.M, (int)g.K, 1});
+        else d.push_back(TnDesc{g.x, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1});
         off += align256(tn_ws_bytes(g.M, g.K, r));
-        d.push_back(TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N});
+        if (drops) dd.push_back(GradDropDesc{g.dy, g.t, at(ws, off), g.dB, DropArgs{}, (int)g.M, (int)g.N, 0});
+        else d.push_back(TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N});
         off += align256(tn_ws_bytes(g.M, g.N, r));
     }
-    if (drop) return launch_tn_batch_dropout(d.data(), dd.data(), (int)d.size(), r, dt_of(dtype), s);
+    if (!dd.empty() && (st = launch_grads_dropout(dd.data(), (int)dd.size(), r, dt_of(dtype), s)) != QLORA_OK) return st;
     return launch_tn_batch(d.data(), (int)d.size(), r, dt_of(dtype), s);
 }
 

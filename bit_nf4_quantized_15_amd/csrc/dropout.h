@@ -109,9 +109,19 @@ __device__ __forceinline__ void drop_tile_rows(f32x16_t& f, const DropArgs& d, u
 // multiples of 2^-16 too).  A null d drops nothing.
 bool drop_args(const qlora_dropout* d, DropArgs* out);
 
-// launch_nt_batch (Y natural) and launch_tn_batch with drop[i] on X of product i
+// launch_nt_batch (Y natural) with drop[i] on X of product i
 qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s);
-qlora_status launch_tn_batch_dropout(const TnDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s);
+// The gradients of layers that drop something: dA = drop(X)^T S into out [D, r], or (dA 0) dB = S^T X into
+// out [r, D]; D below kGradMaxWidth.  ws: tn_ws_bytes(M, D, r) bytes that need no clearing.
+struct GradDropDesc {
+    const uint16_t* X;
+    const uint16_t* S;
+    void* ws;
+    float* out;
+    DropArgs drop;
+    int M, D, dA;
+};
+qlora_status launch_grads_dropout(const GradDropDesc* d, int count, int r, int dt, hipStream_t s);
 // launch_gemm_bwd_dx and the int8 product with drop (thr > 0) on u A^T
 qlora_status launch_gemm_bwd_dx_dropout(const uint16_t* dy, const uint8_t* codes, const uint8_t* q8, const float* a2,
                                         int cb, int dt, const uint16_t* u, const uint16_t* A, const DropArgs& drop,

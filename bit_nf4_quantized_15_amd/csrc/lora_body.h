@@ -289,10 +289,9 @@ struct TnProb {
     float* out;
     int M, D, r, chunk, tiles, splits;
     int64_t ld_d, ld_j;
-    DropArgs drop;      // of X, in kernels with dropout: then out is drop(X)^T S (thr 0: X^T S)
 };
 
-template <int TQ, bool VEC, int NST, int DT, bool DROP = false>
+template <int TQ, bool VEC, int NST, int DT>
 __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
     const uint16_t* __restrict__ X = pr.X;
     const uint16_t* __restrict__ S = pr.S;
@@ -343,13 +342,6 @@ __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
         }
     }
     auto store_x = [&](bf16x8 (&src)[4], int buf, [[maybe_unused]] int st) {
-        if (DROP && pr.drop.thr) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                src[i] = __builtin_bit_cast(bf16x8, drop8(__builtin_bit_cast(u32x4_t, src[i]), pr.drop,
-                                                          (uint32_t)(d0 + lc + 8 * i) >> 3,
-                                                          (uint32_t)(m_begin + kTnRows * st + lr)));
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<bf16x8*>(&tile[buf][lr * kTnLd + lc + 8 * i]) = src[i];
     };
@@ -401,7 +393,7 @@ __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             const int d = d0 + 32 * wave + 8 * (v >> 2) + 4 * h + (v & 3);
-            if (d < D) pr.out[(int64_t)d * pr.ld_d + (int64_t)j * pr.ld_j] = DROP ? acc[q][v] * pr.drop.inv : acc[q][v];
+            if (d < D) pr.out[(int64_t)d * pr.ld_d + (int64_t)j * pr.ld_j] = acc[q][v];
         }
     }
 }

@@ -1,7 +1,5 @@
-// The LoRA products of a training step with dropout (dropout.h): t = s drop(x) A (lora_prep.h) and
-// dA = drop(x)^T u beside dB = t^T dy for several layers in one launch (lora_body.h).  A lane
-// holds 8 consecutive columns of a row of x, the unit of the generator, and masks them in
-// registers between the load and the MFMA operand (t) or the LDS tile (dA).
+// The LoRA branch's product with dropout (dropout.h), t = s drop(x) A of several layers in one launch
+// (lora_prep.h), and the generator's arguments.
 #include <cmath>
 #include <vector>
 
@@ -31,29 +29,6 @@ template <int TQ, bool VEC, int DT>
 __global__ __launch_bounds__(256, TQ <= 2 ? 2 : 1) void down_stream_kernel(const StreamArgs a) {
     stream_body<TQ, VEC, true, true, false, DT>(a);
 }
-
-template <int TQ, bool VEC, int NST, int DT>
-__global__ __launch_bounds__(256, TQ <= 2 && VEC ? 2 : 1) void tnb_dropout_kernel(const TnBatch bt) {
-    const int b = blockIdx.x;
-    int i = 0;
-    while (i + 1 < bt.n && b >= bt.first[i + 1]) ++i;
-    const int c = b - bt.first[i];
-    tn_body<TQ, VEC, NST, DT, true>(bt.p[i], c % bt.p[i].tiles, c / bt.p[i].tiles);
-}
-
-struct TnDropLaunch {
-    const TnBatch& b;
-    unsigned n;
-    hipStream_t s;
-    template <int TQ, bool V, int NST, int DT>
-    void operator()() const {
-        hipLaunchKernelGGL((tnb_dropout_kernel<TQ, V, NST, DT>), dim3(n), dim3(256), 0, s, b);
-    }
-};
-
-}  // namespace
-
-namespace {
 
 // n <= kStreamItems products
 qlora_status down_stream(const NtDesc* d, const DropArgs* drop, int n, int r, int dt, hipStream_t s) {
@@ -108,23 +83,6 @@ qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int 
         st = down_stream(rest.data() + i, rest_drop.data() + i, (int)std::min<size_t>(kStreamItems, rest.size() - i), r, dt,
                          s);
     return st;
-}
-
-qlora_status launch_tn_batch_dropout(const TnDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s) {
-    for (int i0 = 0; i0 < count; i0 += kTnBatch) {
-        TnBatch b{};
-        bool vec = false;
-        int chunk = 64;
-        unsigned total = 0;
-        const qlora_status st = tn_batch(d + i0, std::min(kTnBatch, count - i0), r, b, vec, chunk, total);
-        if (st != QLORA_OK) return st;
-        for (int i = 0; i < b.n; ++i) b.p[i].drop = drop[i0 + i];
-        const TnDropLaunch go{b, total, s};
-        tn_dispatch(r, vec, chunk, dt, go);
-        const qlora_status ls = launch_status();
-        if (ls != QLORA_OK) return ls;
-    }
-    return QLORA_OK;
 }
 
 }  // namespace qlora

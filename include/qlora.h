@@ -500,7 +500,9 @@ qlora_status qlora_lora_down_batch_dropout(const qlora_lora_prod* items, const q
                                            float alpha, int dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* qlora_lora_grads_batch with dropout: dA = drop_i(x)^T u, dB = t^T dy.  drops: an array of
- * count.  Workspace and errors as qlora_lora_grads_batch; drops NULL -> INVALID_ARG. */
+ * count.  The order of fp32 sums depends on the layers of the call, as above.  Workspace and
+ * errors as qlora_lora_grads_batch; drops NULL -> INVALID_ARG; N or K of 2^22 or more of a layer
+ * that drops something -> UNSUPPORTED_SHAPE. */
 qlora_status qlora_lora_grads_batch_dropout(const qlora_lora_grads* layers, const qlora_dropout* drops, int count,
                                             int r, int dtype, void* ws, size_t ws_bytes, void* stream);
 

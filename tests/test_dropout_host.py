@@ -87,6 +87,10 @@ def test_batch_arguments(q):
     for C in (2 ** 31 - 64, 2 ** 31 - 1024):       # columns that the kernel could not count in 32 bits
         wide = (q.LoraProd * 2)(q.LoraProd(FAKE, FAKE, FAKE, 4, 128), q.LoraProd(FAKE, FAKE, FAKE, 4, C))
         assert down(D(0.0, 0.1), items=wide) == SHAPE
+    for N, K in ((64, 2 ** 22), (2 ** 22, 128)):
+        wide = (q.LoraGrads * 2)(q.LoraGrads(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 128),
+                                 q.LoraGrads(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, N, K))
+        assert grads(D(0.0, 0.1), items=wide) == SHAPE
 
 
 def test_the_class(q):

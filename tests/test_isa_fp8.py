@@ -20,7 +20,7 @@ from test_isa_waits import _descriptor, _kernels
 
 pytestmark = pytest.mark.skipif(not os.path.exists(build.HIPCC) and shutil.which("hipcc") is None,
                                 reason="hipcc not available")
-SOURCES = ("fp8_gemm", "fp8_gemv", "fp8_prep", "fp8_quant", "lora_dropout", "gemm_dx_dropout", "int8_gemm_dx_dropout")
+SOURCES = ("fp8_gemm", "fp8_gemv", "fp8_prep", "fp8_quant", "lora_dropout", "lora_grads_dropout", "gemm_dx_dropout", "int8_gemm_dx_dropout")
 
 
 @pytest.fixture(scope="module")
@@ -101,8 +101,8 @@ def test_publication_waits_for_the_payload(asm):
                 n += 1
             assert not any(l.startswith("buffer_wbl2") for l in body), f"{name}: L2 write-back"
         counts[src] = n
-    assert counts["fp8_gemm"] == 18 and counts["fp8_gemv"] == 4 and counts["lora_dropout"] > 0
-    assert counts["fp8_prep"] == counts["fp8_quant"] == counts["gemm_dx_dropout"] == 0
+    assert counts["fp8_gemm"] == 18 and counts["fp8_gemv"] == 4 and counts["lora_grads_dropout"] == 20
+    assert counts["fp8_prep"] == counts["lora_dropout"] == counts["fp8_quant"] == counts["gemm_dx_dropout"] == 0
 
 
 # bytes of scratch a lane, at most, by kernel and first template arguments: masks in the epilogue of the 256 x 256 input
@@ -122,7 +122,7 @@ def test_registers_and_scratch(asm):
             assert d["amdhsa_group_segment_fixed_size"] <= 160 * 1024, name
             used = d["amdhsa_private_segment_fixed_size"]
             if used:
-                kernel = re.search(r"\d+((?:fp8|down|tnb|nf4|int8|prep)_\w+?_kernel)", name).group(1)
+                kernel = re.search(r"\d+((?:fp8|down|grads|nf4|int8|prep)_\w+?_kernel)", name).group(1)
                 found[name] = (used, max([v for (k, a), v in SCRATCH.items()
                                           if k == kernel and tuple(_args(name)[:len(a)]) == a], default=0))
     bad = {k: v for k, v in found.items() if v[0] > v[1]}
