@@ -8,6 +8,8 @@
 //    512 columns, so that the scale bytes of neighbouring rows, which lie side by side, are
 //    written together and four blocks' loads are in flight.
 //  - weights (128 x 128): a workgroup takes a block, 8 loads of 16 bytes in flight per lane.
+// Traced, bf16 28672 x 8192: 147 us (4.8 TB/s read and written), and back 118 us (6.0 TB/s, of codes partly
+// in the caches); 77 x 4096 rows: 3.3 and 2.7 us, a launch and one load's latency.
 #include "fp8.h"
 
 namespace qlora {

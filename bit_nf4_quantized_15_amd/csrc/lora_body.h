@@ -1,5 +1,5 @@
-// Bodies of the LoRA side-path kernels, shared by the kernels without dropout (lora.hip) and
-// those with it (lora_dropout.hip).
+// Bodies of the LoRA side-path kernels (lora.hip), whose loads and operand reads the products with
+// a preparation or with dropout use too (lora_prep.h).
 #pragma once
 
 #include "common.h"

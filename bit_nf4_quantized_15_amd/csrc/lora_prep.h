@@ -6,10 +6,15 @@
 // on their way while one is multiplied.  A wave loads whole 256-byte pieces of its 32 rows, 16
 // lanes to a row, so that a row's maximum over the block is a rotation within the lanes' DPP row and
 // its codes are one 128-byte store; what the mask leaves goes through LDS of the wave's own into
-// MFMA operands.  Y's rows go through LDS for all four waves.  Where C is split, the fp32 sums of each range go to the
-// workspace and a second kernel adds them in order, on all CUs.  (Adding them in the launch, by the
+// MFMA operands.  Y's rows go through LDS for all four waves.  Where C is split, the fp32 sums of
+// each range go to the workspace and a second kernel adds them in order, on all CUs.  (Adding them in the launch, by the
 // workgroup of the last range as lora_body.h does, left that to one CU per 128 tokens: 333 x
 // 11008, r = 8 took 24 us, 4096 x 11008, r = 64 38 us.)
+//
+// Traced, us, the pass and the second kernel: x 8192 x 8192, r = 64, dropout, with codes 56 + 7 (HBM: 4.0
+// TB/s in the pass); dy 4096 x 11008, r = 64, with codes 32 + 5; x 333 x 11008, r = 8, dropout, with
+// codes 8.8 + 4.4, latencies; t of three layers that share x 4096 x 4096, r = 64, dropout, 25 + 7:
+// the generator's 12 us of every SIMD's time in the pass, whose x comes from the caches twice.
 #pragma once
 
 #include "fp8.h"

@@ -32,4 +32,6 @@ Modules:
   merge  -- the LoRA merge W_eff = W_hat + (alpha/r) (A B)^T for deployment
   fp4    -- the fp4 quant type: E2M1 4-bit float levels / 6 in the same scheme
   int8   -- int8 codes with one scale per row, and the layer on them
+  fp8    -- e4m3 codes with a power-of-two scale per block, and the layer on them
+  dropout -- the counter-based generator, the mask, and the LoRA branch's products with it
 """
