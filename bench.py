@@ -74,6 +74,9 @@ KERNELS = {"fwd": "nf4_gemm_fwd_kernel", "bwd_dx": "nf4_gemm_bwd_dx_kernel", "qu
            "gemv": "nf4_gemv_stream_kernel", "grads": "tnb_kernel"}
 _CSRC = os.path.join(HERE, "bit_nf4_quantized_15_amd", "csrc")
 SOURCES = {"fwd": "gemm.hip", "bwd_dx": "gemm.hip", "quantize": "quantize.hip", "gemv": "gemv.hip", "grads": "lora.hip"}
+# headers with bodies of the kernels in these sources (read where they lie, whatever _CSRC is)
+BODIES = {"gemm.hip": ("gemm_tile.h", "gemm_dx.h"), "lora.hip": ("lora_body.h",)}
+_BODY_DIR = _CSRC
 WORKLOAD_TAG = {"fwd": "7B_block_7_layers_M4096_r64", "bwd_dx": "7B_block_7_layers_M4096_r64",
                 "quantize": "7B_block_7_layers", "gemv": "gate_up_2x11008x4096_M1_r32",
                 "grads": "7B_block_7_layers_M4096_r64"}
@@ -87,11 +90,14 @@ DECODE_SHAPES = {"q_proj": ([4096], 4096, 16), "qkv": ([4096] * 3, 4096, 16), "g
 
 
 def gemm_source_sha(kind="fwd"):
-    """sha256 of a kernel's source with comments and whitespace removed: a change of
-    the code (not of its comments) invalidates the recorded counter figures."""
+    """sha256 of a kernel's source, and of the headers with its body, with comments and whitespace
+    removed: a change of the code (not of its comments) invalidates the recorded counter figures."""
     import re
     with open(os.path.join(_CSRC, SOURCES[kind])) as f:
         text = f.read()
+    for name in BODIES.get(SOURCES[kind], ()):
+        with open(os.path.join(_BODY_DIR, name)) as f:
+            text += "\n" + f.read()
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     text = re.sub(r"//[^\n]*", " ", text)
     return hashlib.sha256(" ".join(text.split()).encode()).hexdigest()

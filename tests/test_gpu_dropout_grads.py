@@ -67,3 +67,22 @@ def test_a_column_that_is_not_finite_stays_alone(q):
         assert bool(torch.isnan(got[k]).all()) == kept
         got[k] = want[k]
         assert torch.equal(got, want)
+
+
+def test_no_tokens(q):
+    """An empty batch through the layers with dropout: empty outputs, zero gradients."""
+    import torch
+    say("[dropout] M=0")
+    N, K, r = 128, 192, 8
+    bf = lambda *s: torch.randn(s, device="cuda:0").to(torch.bfloat16)
+    A, B, W, x, dy = bf(K, r), bf(r, N), bf(N, K), bf(0, K), bf(0, N)
+    drop = q.Dropout(0.1, SEED, OFFSET)
+    w4, w8, wf = q.quantize(W), q.int8_quantize(W), q.fp8_quantize(W)
+    for fwd, w in ((q.linear_fwd, w4), (q.int8_linear_fwd, w8), (q.fp8_linear_fwd, wf)):
+        y, t = fwd(w, x, A, B, 16.0, dropout=drop)
+        assert tuple(y.shape) == (0, N) and tuple(t.shape) == (0, r)
+    for bwd, w in ((q.linear_bwd_dx, w4), (q.int8_linear_bwd_dx, w8), (q.fp8_linear_bwd_dx, wf)):
+        u, dx = bwd(w, A, B, 16.0, dy, dropout=drop)
+        assert tuple(u.shape) == (0, r) and tuple(dx.shape) == (0, K)
+    dx, dA, dB = q.linear_bwd(w4, x, A, B, 16.0, dy, dropout=drop)
+    assert tuple(dx.shape) == (0, K) and not dA.any() and not dB.any()
