@@ -299,7 +299,7 @@ __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
     constexpr int kTnMaxChunk = TQ <= 3 ? 512 : 256;  // = tn_max_chunk(r) for r in (32 (TQ-1), 32 TQ]
     static_assert(NST * kTnRows <= kTnMaxChunk, "steps beyond the slice");
     constexpr int kSLd = slice_ld<TQ>();
-        constexpr int kCh = 4 * TQ;                       // 16-byte chunks per slice row
+    constexpr int kCh = 4 * TQ;                       // 16-byte chunks per slice row
     // An 8-step split holds its slice of S in LDS in two phases of 256 rows (the second
     // stored after step 3), so that at r <= 64 a workgroup takes 80 KB and two share a CU.
     constexpr int kSH = NST > 4 ? 2 : 1;
@@ -313,7 +313,7 @@ __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
     const int m_begin = split * chunk;
     const int m_end = min(M, m_begin + chunk);
 
-        bf16x8 sv[kSH][kSPer];
+    bf16x8 sv[kSH][kSPer];
     {
         const rsrc_t srs = buf_rsrc(S + (int64_t)m_begin * r, (uint64_t)(m_end - m_begin) * r * 2);
 #pragma unroll
@@ -364,7 +364,7 @@ __device__ __forceinline__ void tn_body(const TnProb& pr, int ti, int split) {
     // A operand = X^T: 8 consecutive m of column d = 32*wave + l32 of the tile.  Step
     // st + 1 goes into the buffer step st - 1 was read from (closed by the barrier).
 #pragma unroll
-        for (int st = 0; st < NST; ++st) {
+    for (int st = 0; st < NST; ++st) {
         const int buf = st & 1;
         constexpr int kHalf = NST / kSH;
         if (kSH == 2 && st == kHalf) {     // every wave is past the first phase (the barrier above)
