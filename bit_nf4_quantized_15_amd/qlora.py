@@ -231,6 +231,11 @@ class Dropout:
                 raise ValueError(f"{name}: expected 0 <= {name} < 2**64, got {v}")
         self.p, self.seed, self.offset = float(p), int(seed), int(offset)
 
+    @property
+    def drops(self):
+        """Whether it drops anything: round(65536 p) > 0."""
+        return round(self.p * 65536) > 0
+
     def state(self):
         return DropoutState(self.seed, self.offset, self.p)
 
@@ -791,10 +796,13 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     """y = sx sw (xq wq^T) + (alpha/r)(x A) B of an int8 weight (qlora_int8_linear_fwd); A = B = None: the int8
     product alone.  keep: an Int8Tensor [M, K] that receives x in 8 bits for the backward.  Returns (y, t or
     None).  With a Dropout the branch takes drop(x) for x (qlora_lora_down_batch_dropout, qlora_int8_quantize,
-    qlora_int8_gemm_fwd)."""
+    qlora_int8_gemm_fwd), and the backward needs the 16-bit x (lora_grads_batch): the gradients from an 8-bit
+    checkpoint apply no mask, so keep is refused."""
     if dropout is not None:
         if A is None or B is None:
             raise ValueError("dropout: a layer without a LoRA branch has none")
+        if keep is not None and dropout.drops:
+            raise ValueError("keep: lora_grads_batch_int8 has no dropout; keep the 16-bit x of a layer that drops")
         cur = torch.cuda.current_device()
         _int8_branch(w, A, B, cur)
         _dev8(x, w.dtype, "x", (x.shape[0], w.cols), cur)
@@ -845,7 +853,7 @@ def int8_gemm_fwd(w, x, t=None, B=None, y=None):
 def int8_linear_bwd_dx(w, A, B, alpha, dy, u=None, dx=None, ws=None, dropout=None):
     """(u, dx) of the int8 layer for upstream dy (qlora_int8_linear_bwd_dx): u = (alpha/r) dy B^T, kept for
     lora_grads_batch_int8, and dx = dy W + u A^T; A = B = None: (None, dy W).  With the forward's Dropout,
-    dy W + drop(u A^T) (qlora_int8_linear_bwd_dx_dropout)."""
+    dy W + drop(u A^T) (qlora_int8_linear_bwd_dx_dropout); u is then for lora_grads_batch with that Dropout."""
     M = dy.shape[0]
     cur = torch.cuda.current_device()
     st = _int8_here(w, "w", cur)
@@ -899,7 +907,8 @@ def int8_gemm_bwd_dx(w, dy, u=None, A=None, dx=None, dropout=None):
 def lora_grads_batch_int8(layers, dA=None, dB=None, ws=None):
     """lora_grads_batch with each layer's x as its 8-bit checkpoint (qlora_lora_grads_batch_int8).  layers: a list
     of (x, t, u, dy), x an Int8Tensor, all of one rank and one dtype; dA, dB: optional lists of output tensors.
-    Returns the lists (dA, dB), fp32."""
+    No layer among them drops anything: lora_grads_batch takes those, with their 16-bit x.  Returns the lists
+    (dA, dB), fp32."""
     n = len(layers)
     if n == 0:
         return [], []

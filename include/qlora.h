@@ -507,7 +507,10 @@ qlora_status qlora_lora_grads_batch_dropout(const qlora_lora_grads* layers, cons
                                             int r, int dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* The input gradient with dropout, dx = dy W_hat^T + drop(u A^T): the calls without it
- * plus drop (NULL -> INVALID_ARG), with their workspaces and errors.  (N, K) as there. */
+ * plus drop (NULL -> INVALID_ARG), with their workspaces and errors.  (N, K) as there.
+ * Their u is for qlora_lora_grads_batch_dropout with the same drop and the 16-bit x, of the int8
+ * layer too: qlora_lora_grads_batch_int8 applies no mask, and its dA of a layer that drops
+ * something would be x^T u. */
 qlora_status qlora_linear_bwd_dx_dropout(const qlora_nf4* w, int64_t M, const uint16_t* A, const uint16_t* B, int r,
                                          float alpha, const qlora_dropout* drop, const uint16_t* dy, uint16_t* u,
                                          uint16_t* dx, void* ws, size_t ws_bytes, void* stream);

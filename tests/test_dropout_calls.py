@@ -1,0 +1,54 @@
+"""The binding's calls with dropout that are made of several library calls, with stand-ins for tensors and for the
+library, without a GPU: which library calls they make, and what they refuse before the first of them."""
+import types
+
+import pytest
+import torch
+
+from test_int8_devices import Fake
+
+BF, F32, U8, I8 = torch.bfloat16, torch.float32, torch.uint8, torch.int8
+M, N, K, R = 3, 40, 64, 8
+
+
+@pytest.fixture
+def q(monkeypatch):
+    """The binding with a library that notes its calls and launches nothing; the current device is cuda:0.  `refuse` names
+    an entry point that reports an unsupported shape."""
+    from bit_nf4_quantized_15_amd import qlora
+    seen = types.SimpleNamespace(q=qlora, calls=[], refuse=None)
+
+    class Lib:
+        def __getattr__(self, name):
+            def f(*a):
+                if name == "qlora_status_string":
+                    return b"refused"
+                if name.endswith("_workspace"):
+                    return 4096
+                seen.calls.append(name)
+                return -2 if name == seen.refuse else 0
+            return f
+
+    monkeypatch.setattr(qlora, "lib", Lib())
+    monkeypatch.setattr(qlora, "empty_hook", lambda *s, dtype, device: Fake(s[0] if isinstance(s[0], tuple) else s, dtype))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    return seen
+
+
+def int8(q, rows, cols=K):
+    t = q.Int8Tensor.__new__(q.Int8Tensor)
+    t.codes, t.scale, t.dtype, t.rows, t.cols = Fake((rows, cols), I8), Fake((rows,), F32), BF, rows, cols
+    return t
+
+
+def test_a_checkpoint_is_not_kept_of_a_layer_that_drops(q):
+    """The gradients from an 8-bit checkpoint know no mask: dA would be that of x, not of drop(x)."""
+    lib = q.q
+    w, x, A, B = int8(lib, N), Fake((M, K), BF), Fake((K, R), BF), Fake((R, N), BF)
+    with pytest.raises(ValueError, match="keep"):
+        lib.int8_linear_fwd(w, x, A, B, 1.0, keep=int8(lib, M), dropout=lib.Dropout(0.1))
+    assert not q.calls
+    for drop in (None, lib.Dropout(0.0), lib.Dropout(0.4 / 65536)):     # nothing is dropped: x is the branch's
+        lib.int8_linear_fwd(w, x, A, B, 1.0, keep=int8(lib, M), dropout=drop)
+    lib.int8_linear_fwd(w, x, A, B, 1.0, dropout=lib.Dropout(0.1))
