@@ -395,10 +395,11 @@ def _ws(nbytes, device, ws):
 
 def linear_fwd(w, x, A, B, alpha, y=None, t=None, want_t=True, ws=None, dropout=None):
     """y = x W_hat + (alpha/r)(x A) B (qlora_linear_fwd).  Returns (y, t or None).  With a Dropout the branch takes
-    drop(x) for x (qlora_lora_down_batch_dropout, then qlora_fused_gemm_fwd)."""
+    drop(x) for x (qlora_lora_down_batch_dropout, then qlora_fused_gemm_fwd); one that drops nothing is None."""
     if dropout is not None:
         _no_f32(w, "linear_fwd")
         _here(x, A, B, w.codes, w.q8, w.a2, y, t, ws)
+    if dropout is not None and dropout.drops:
         _dev(B, w.dtype, "B", (A.shape[1], w.N))
         _dev(x, w.dtype, "x", (x.shape[0], w.K))
         _dev(A, w.dtype, "A", (w.K, A.shape[1]))
@@ -506,10 +507,12 @@ def fused_gemm_bwd_dx(w, dy, u, A, dx=None, dropout=None):
 
 def linear_bwd(w, x, A, B, alpha, dy, t=None, need_dx=True, dx=None, dA=None, dB=None, ws=None, dropout=None):
     """(dx, dA, dB) of the layer for upstream dy (qlora_linear_bwd); dx is None when not needed.  With the forward's
-    Dropout: its three stages (u and dx, then the gradients of drop(x); a t not given is computed again)."""
+    Dropout: its three stages (u and dx, then the gradients of drop(x); a t not given is computed again); one that
+    drops nothing is None."""
     if dropout is not None:
         _no_f32(w, "linear_bwd")
         _here(x, A, B, dy, t, w.codes, w.q8, w.a2, dx, dA, dB, ws)
+    if dropout is not None and dropout.drops:
         _dev(x, w.dtype, "x", (x.shape[0], w.K))
         _dev(A, w.dtype, "A", (w.K, A.shape[1]))
         _dev(B, w.dtype, "B", (A.shape[1], w.N))
@@ -797,11 +800,11 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     product alone.  keep: an Int8Tensor [M, K] that receives x in 8 bits for the backward.  Returns (y, t or
     None).  With a Dropout the branch takes drop(x) for x (qlora_lora_down_batch_dropout, qlora_int8_quantize,
     qlora_int8_gemm_fwd), and the backward needs the 16-bit x (lora_grads_batch): the gradients from an 8-bit
-    checkpoint apply no mask, so keep is refused."""
-    if dropout is not None:
-        if A is None or B is None:
-            raise ValueError("dropout: a layer without a LoRA branch has none")
-        if keep is not None and dropout.drops:
+    checkpoint apply no mask, so keep is refused.  A Dropout that drops nothing is None."""
+    if dropout is not None and (A is None or B is None):
+        raise ValueError("dropout: a layer without a LoRA branch has none")
+    if dropout is not None and dropout.drops:
+        if keep is not None:
             raise ValueError("keep: lora_grads_batch_int8 has no dropout; keep the 16-bit x of a layer that drops")
         cur = torch.cuda.current_device()
         _int8_branch(w, A, B, cur)

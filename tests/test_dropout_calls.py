@@ -52,3 +52,30 @@ def test_a_checkpoint_is_not_kept_of_a_layer_that_drops(q):
     for drop in (None, lib.Dropout(0.0), lib.Dropout(0.4 / 65536)):     # nothing is dropped: x is the branch's
         lib.int8_linear_fwd(w, x, A, B, 1.0, keep=int8(lib, M), dropout=drop)
     lib.int8_linear_fwd(w, x, A, B, 1.0, dropout=lib.Dropout(0.1))
+
+
+def nf4(lib, dtype=BF):
+    return lib.NF4Weight(Fake((N * K // 2,), U8), Fake((N * K // 64,), U8), Fake((1,), F32), N, K, dtype=dtype)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.4 / 65536])
+def test_a_dropout_that_drops_nothing_is_the_call_without(q, p):
+    lib = q.q
+    w4, w8 = nf4(lib), int8(lib, N)
+    x, A, B, dy, t = Fake((M, K), BF), Fake((K, R), BF), Fake((R, N), BF), Fake((M, N), BF), Fake((M, R), BF)
+    for f in (lambda d: lib.linear_fwd(w4, x, A, B, 1.0, dropout=d),
+              lambda d: lib.linear_fwd(w4, x, A, B, 1.0, t=t, want_t=False, dropout=d),
+              lambda d: lib.linear_bwd(w4, x, A, B, 1.0, dy, dropout=d),
+              lambda d: lib.linear_bwd(w4, x, A, B, 1.0, dy, t=t, need_dx=False, dropout=d),
+              lambda d: lib.int8_linear_fwd(w8, x, A, B, 1.0, dropout=d),
+              lambda d: lib.int8_linear_fwd(w8, x, A, B, 1.0, want_t=False, dropout=d)):
+        f(None)
+        plain = list(q.calls)
+        q.calls.clear()
+        got, want = f(lib.Dropout(p, 1, 2)), f(None)
+        assert q.calls == plain * 2
+        assert [v is None for v in got] == [v is None for v in want]
+        q.calls.clear()
+    for f in (lib.linear_fwd, lambda *a, **kw: lib.linear_bwd(*a, dy, **kw)):    # offered for the 16-bit dtypes all the same
+        with pytest.raises(TypeError):
+            f(nf4(lib, F32), x, A, B, 1.0, dropout=lib.Dropout(p))
