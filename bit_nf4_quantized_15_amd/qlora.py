@@ -260,6 +260,16 @@ def _here(*tensors):
             raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{cur}")
 
 
+def _aligned(where, *tensors):
+    """Of a call that makes several: their tensors' alignment, before the first of them is made, so that one that is
+    refused leaves every output as it was."""
+    if any(t is not None and t.data_ptr() % 16 for t in tensors):
+        raise QLoraError(-3, where)
+
+
+GRADS_DROPOUT_WIDTH = 1 << 22      # N and K of qlora_lora_grads_batch_dropout lie below
+
+
 def sizes(N, K):
     """(codes bytes, q8 bytes, a2 bytes) of an [N, K] quantized weight."""
     cb, qb, ab = c_sz(), c_sz(), c_sz()
@@ -400,9 +410,19 @@ def linear_fwd(w, x, A, B, alpha, y=None, t=None, want_t=True, ws=None, dropout=
         _no_f32(w, "linear_fwd")
         _here(x, A, B, w.codes, w.q8, w.a2, y, t, ws)
     if dropout is not None and dropout.drops:
-        _dev(B, w.dtype, "B", (A.shape[1], w.N))
-        _dev(x, w.dtype, "x", (x.shape[0], w.K))
-        _dev(A, w.dtype, "A", (w.K, A.shape[1]))
+        M, r = x.shape[0], A.shape[1]
+        _dev(B, w.dtype, "B", (r, w.N))
+        _dev(x, w.dtype, "x", (M, w.K))
+        _dev(A, w.dtype, "A", (w.K, r))
+        if y is not None:
+            _dev(y, w.dtype, "y", (M, w.N))
+        if t is not None:
+            _dev(t, w.dtype, "t", (M, r))
+        if M:
+            _aligned("linear_fwd", x, A, B, y, t)
+        # (the product of no rows: its checks of the weight, before t is written)
+        _check(lib.qlora_fused_gemm_fwd(ctypes.byref(w.state()), None, 0, None, None, r, None, _stream()),
+               "qlora_fused_gemm_fwd")
         t = lora_down(x, A, alpha, t=t, ws=ws, dropout=dropout)
         return fused_gemm_fwd(w, x, t, B, y=y), (t if want_t else None)
     M, K = x.shape
@@ -513,10 +533,17 @@ def linear_bwd(w, x, A, B, alpha, dy, t=None, need_dx=True, dx=None, dA=None, dB
         _no_f32(w, "linear_bwd")
         _here(x, A, B, dy, t, w.codes, w.q8, w.a2, dx, dA, dB, ws)
     if dropout is not None and dropout.drops:
-        _dev(x, w.dtype, "x", (x.shape[0], w.K))
-        _dev(A, w.dtype, "A", (w.K, A.shape[1]))
-        _dev(B, w.dtype, "B", (A.shape[1], w.N))
-        _dev(dy, w.dtype, "dy", (x.shape[0], w.N))
+        M, r = x.shape[0], A.shape[1]
+        for v, dt, name, shape in ((x, w.dtype, "x", (M, w.K)), (A, w.dtype, "A", (w.K, r)), (B, w.dtype, "B", (r, w.N)),
+                                   (dy, w.dtype, "dy", (M, w.N)), (t, w.dtype, "t", (M, r)),
+                                   (dx if need_dx else None, w.dtype, "dx", (M, w.K)),
+                                   (dA, torch.float32, "dA", (w.K, r)), (dB, torch.float32, "dB", (r, w.N))):
+            if v is not None:
+                _dev(v, dt, name, shape)
+        if M:
+            _aligned("linear_bwd", x, A, B, dy, t, dx if need_dx else None, dA, dB, ws)
+            if max(w.N, w.K) >= GRADS_DROPOUT_WIDTH:
+                raise QLoraError(-2, "linear_bwd")
         if need_dx:
             u, dx = linear_bwd_dx(w, A, B, alpha, dy, dx=dx, ws=ws, dropout=dropout)
         else:
@@ -806,11 +833,22 @@ def int8_linear_fwd(w, x, A=None, B=None, alpha=0.0, y=None, t=None, want_t=True
     if dropout is not None and dropout.drops:
         if keep is not None:
             raise ValueError("keep: lora_grads_batch_int8 has no dropout; keep the 16-bit x of a layer that drops")
-        cur = torch.cuda.current_device()
-        _int8_branch(w, A, B, cur)
-        _dev8(x, w.dtype, "x", (x.shape[0], w.cols), cur)
+        M, cur = x.shape[0], torch.cuda.current_device()
+        st, r = _int8_here(w, "w", cur), _int8_branch(w, A, B, cur)
+        _dev8(x, w.dtype, "x", (M, w.cols), cur)
+        if y is not None:
+            _dev8(y, w.dtype, "y", (M, w.rows), cur)
+        if t is not None:
+            _dev8(t, w.dtype, "t", (M, r), cur)
+        _here(ws)
+        if M:
+            _aligned("int8_linear_fwd", x, A, B, y, t)
+        # (the product of no rows: its checks of the weight, before t is written)
+        none = Int8State(None, None, 0, w.cols, DTYPES[w.dtype])
+        _check(lib.qlora_int8_gemm_fwd(st, ctypes.byref(none), None, None, r, None, _stream8(cur)),
+               "qlora_int8_gemm_fwd")
         t = lora_down(x, A, alpha, t=t, ws=ws, dropout=dropout)
-        return int8_gemm_fwd(w, int8_quantize(x, out=keep), t, B, y=y), (t if want_t else None)
+        return int8_gemm_fwd(w, int8_quantize(x), t, B, y=y), (t if want_t else None)
     M = x.shape[0]
     cur = torch.cuda.current_device()
     st = _int8_here(w, "w", cur)
