@@ -406,14 +406,6 @@ __global__ __launch_bounds__(kT, 1) void nf4_gemm_fwd_kernel(
     }
 }
 
-template <bool DYVEC, bool DQ, int CB, int DT>
-__global__ __launch_bounds__(kT8, 1) void nf4_gemm_bwd_dx_kernel(
-    const uint16_t* __restrict__ dy, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ q8,
-    const float* __restrict__ a2, const uint16_t* __restrict__ u_, const uint16_t* __restrict__ Al,
-    uint16_t* __restrict__ dx, int M, int N, int K, int r, int tiles_m, int tiles_k) {
-    gemm_bwd_dx_body<DYVEC, DQ, CB, DT, false>(dy, codes, q8, a2, u_, Al, dx, M, N, K, r, tiles_m, tiles_k, DropArgs{});
-}
-
 }  // namespace
 
 qlora_status launch_gemm_fwd(const uint16_t* x, const uint8_t* codes, const uint8_t* q8, const float* a2, int cb,
@@ -458,8 +450,8 @@ qlora_status launch_gemm_bwd_dx(const uint16_t* dy, const uint8_t* codes, const 
     with_cb_dt(cb, dt, [&](auto cbc, auto dtc) {
         constexpr int CB = decltype(cbc)::value, DT = decltype(dtc)::value;
 #define QL_BWD(V, DQ)                                                                                           \
-    hipLaunchKernelGGL((nf4_gemm_bwd_dx_kernel<V, DQ, CB, DT>), dim3(tm * tk), dim3(kT8), 0, s, dy, codes, q8, a2, u, \
-                       A, dx, M, N, K, r, tm, tk)
+    hipLaunchKernelGGL((nf4_gemm_bwd_dx_kernel<V, DQ, CB, DT, NoDrop>), dim3(tm * tk), dim3(kT8), 0, s, dy, codes, q8, a2, u, \
+                       A, dx, M, N, K, r, tm, tk, NoDrop{})
         if (q8) {
             if (vec) QL_BWD(true, true); else QL_BWD(false, true);
         } else {
