@@ -4,7 +4,6 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <vector>
 
 #include "common.h"
 #include "dropout.h"
@@ -371,10 +370,26 @@ size_t qlora_lora_prod_batch_workspace(const qlora_lora_prod* items, int count, 
     return total;
 }
 
+// The generator's arguments of item i; drops NULL: nothing is dropped.
+static DropArgs drop_of(const qlora_dropout* drops, int i) {
+    DropArgs d;
+    drop_args(drops ? drops + i : nullptr, &d);
+    return d;
+}
+static bool good_drops(const qlora_dropout* drops, int count) {
+    DropArgs d;
+    for (int i = 0; i < count; ++i)
+        if (!drop_args(drops + i, &d)) return false;
+    return true;
+}
+
+// Products, and contractions, of a launch.
+constexpr int kProducts = 8, kContractions = 16;
+
 // t_i = s x_i A_i (y_natural) or u_i = s dy_i B_i^T for every item, in launches of up to 8.
-// drop (nullable): count of them, on the items' x.
-static qlora_status lora_prod_batch(const qlora_lora_prod* items, const DropArgs* drop, int count, int r, float alpha,
-                                    int dtype, bool y_natural, void* ws, size_t ws_bytes, void* stream) {
+// drops (nullable): count good ones, on the items' x.
+static qlora_status lora_prod_batch(const qlora_lora_prod* items, const qlora_dropout* drops, int count, int r,
+                                    float alpha, int dtype, bool y_natural, void* ws, size_t ws_bytes, void* stream) {
     if (count < 0 || r < 1 || r > 128 || !std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
     if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F16) return QLORA_ERR_INVALID_ARG;
     if (count == 0) return QLORA_OK;
@@ -384,7 +399,7 @@ static qlora_status lora_prod_batch(const qlora_lora_prod* items, const DropArgs
         if (bad_dims(e.M, 1, e.C, r)) return QLORA_ERR_INVALID_ARG;
         if (y_natural && e.C % kBlock) return QLORA_ERR_UNSUPPORTED_SHAPE;
         // (the kernel with dropout counts columns in 32 bits, up to some blocks past the last)
-        if (drop && drop[i].thr && e.C > INT32_MAX - 1024) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        if (e.C > INT32_MAX - 1024 && drop_of(drops, i).thr) return QLORA_ERR_UNSUPPORTED_SHAPE;
         if (e.M == 0) continue;
         if (!e.x || !e.w || !e.out) return QLORA_ERR_INVALID_ARG;
         if (!aligned16(e.x) || !aligned16(e.w) || !aligned16(e.out)) return QLORA_ERR_MISALIGNED;
@@ -392,20 +407,32 @@ static qlora_status lora_prod_batch(const qlora_lora_prod* items, const DropArgs
     const size_t need = qlora_lora_prod_batch_workspace(items, count, r);
     if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
-    std::vector<NtDesc> d;
-    std::vector<DropArgs> dd;
-    d.reserve((size_t)count);
-    size_t off = 0;
-    for (int i = 0; i < count; ++i) {
-        const qlora_lora_prod& e = items[i];
-        if (e.M == 0) continue;
-        if (drop) dd.push_back(drop[i]);
-        d.push_back(NtDesc{e.x, e.w, at(ws, off), e.out, alpha / (float)r, (int)e.M, (int)e.C});
-        off += align256(nt_ws_bytes(e.M, e.C, r));
+    // Items that drop nothing first (the products of the call without dropout, bit for bit), then the
+    // others: whole launches of each, gathered in fixed arrays.
+    for (int dropping = 0; dropping < (drops ? 2 : 1); ++dropping) {
+        NtDesc d[kProducts];
+        DropArgs dd[kProducts];
+        int n = 0;
+        size_t off = 0;
+        for (int i = 0; i <= count; ++i) {
+            if (n == kProducts || (i == count && n)) {
+                const qlora_status st =
+                    dropping ? launch_nt_batch_dropout(d, dd, n, r, dt_of(dtype), (hipStream_t)stream)
+                             : launch_nt_batch(d, n, y_natural, r, dt_of(dtype), (hipStream_t)stream);
+                if (st != QLORA_OK) return st;
+                n = 0;
+            }
+            if (i == count || items[i].M == 0) continue;
+            const qlora_lora_prod& e = items[i];
+            const DropArgs drop = drop_of(drops, i);
+            if ((drop.thr != 0) == (dropping != 0)) {
+                dd[n] = drop;
+                d[n++] = NtDesc{e.x, e.w, at(ws, off), e.out, alpha / (float)r, (int)e.M, (int)e.C};
+            }
+            off += align256(nt_ws_bytes(e.M, e.C, r));
+        }
     }
-    if (d.empty()) return QLORA_OK;
-    if (drop) return launch_nt_batch_dropout(d.data(), dd.data(), (int)d.size(), r, dt_of(dtype), (hipStream_t)stream);
-    return launch_nt_batch(d.data(), (int)d.size(), y_natural, r, dt_of(dtype), (hipStream_t)stream);
+    return QLORA_OK;
 }
 
 qlora_status qlora_lora_down_batch(const qlora_lora_prod* items, int count, int r, float alpha, int dtype, void* ws,
@@ -413,25 +440,10 @@ qlora_status qlora_lora_down_batch(const qlora_lora_prod* items, int count, int 
     return lora_prod_batch(items, nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
 }
 
-// The generator's arguments of each item; any: whether some item drops anything.
-static bool drops_of(const qlora_dropout* drops, int count, std::vector<DropArgs>& out, bool& any) {
-    any = false;
-    for (int i = 0; i < count; ++i) {
-        DropArgs d;
-        if (!drop_args(drops + i, &d)) return false;
-        any = any || d.thr;
-        out.push_back(d);
-    }
-    return true;
-}
-
 qlora_status qlora_lora_down_batch_dropout(const qlora_lora_prod* items, const qlora_dropout* drops, int count, int r,
                                            float alpha, int dtype, void* ws, size_t ws_bytes, void* stream) {
-    if (count <= 0) return lora_prod_batch(items, nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
-    std::vector<DropArgs> d;
-    bool any;
-    if (!drops || !drops_of(drops, count, d, any)) return QLORA_ERR_INVALID_ARG;
-    return lora_prod_batch(items, any ? d.data() : nullptr, count, r, alpha, dtype, true, ws, ws_bytes, stream);
+    if (count > 0 && (!drops || !good_drops(drops, count))) return QLORA_ERR_INVALID_ARG;
+    return lora_prod_batch(items, drops, count, r, alpha, dtype, true, ws, ws_bytes, stream);
 }
 
 qlora_status qlora_lora_u_batch(const qlora_lora_prod* items, int count, int r, float alpha, int dtype, void* ws,
@@ -453,8 +465,9 @@ size_t qlora_lora_grads_batch_workspace(const qlora_lora_grads* layers, int coun
     return total;
 }
 
-static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const DropArgs* drop, int count, int r, int dtype,
-                                     void* ws, size_t ws_bytes, void* stream) {
+// drops (nullable): count good ones, on the layers' x.
+static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const qlora_dropout* drops, int count, int r,
+                                     int dtype, void* ws, size_t ws_bytes, void* stream) {
     if (count < 0 || r < 1 || r > 128) return QLORA_ERR_INVALID_ARG;
     if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F16) return QLORA_ERR_INVALID_ARG;
     if (count == 0) return QLORA_OK;
@@ -467,35 +480,49 @@ static qlora_status lora_grads_batch(const qlora_lora_grads* layers, const DropA
         if (g.M == 0) continue;
         if (!g.x || !g.t || !g.u || !g.dy) return QLORA_ERR_INVALID_ARG;
         if (!aligned16(g.x) || !aligned16(g.t) || !aligned16(g.u) || !aligned16(g.dy)) return QLORA_ERR_MISALIGNED;
-        if (drop && drop[i].thr && (g.N >= kGradMaxWidth || g.K >= kGradMaxWidth)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+        if ((g.N >= kGradMaxWidth || g.K >= kGradMaxWidth) && drop_of(drops, i).thr) return QLORA_ERR_UNSUPPORTED_SHAPE;
     }
     const size_t need = qlora_lora_grads_batch_workspace(layers, count, r);
     if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
     hipStream_t s = (hipStream_t)stream;
-    std::vector<TnDesc> d;            // (layers that drop nothing: the call without dropout, bit for bit)
-    std::vector<GradDropDesc> dd;
-    d.reserve(2 * (size_t)count);
-    size_t off = 0;
-    qlora_status st = QLORA_OK;
+    qlora_status st;
     for (int i = 0; i < count; ++i) {
         const qlora_lora_grads& g = layers[i];
-        if (g.M == 0) {  // empty sums
-            if ((st = launch_fill(g.dA, g.K * r, 0.0f, s)) != QLORA_OK) return st;
-            if ((st = launch_fill(g.dB, (int64_t)r * g.N, 0.0f, s)) != QLORA_OK) return st;
-            continue;
-        }
-        // dA [K, r] = x^T u ; dB [r, N] = t^T dy, stored transposed from the [N, r] reduction
-        const bool drops = drop && drop[i].thr;
-        if (drops) dd.push_back(GradDropDesc{g.x, g.u, at(ws, off), g.dA, drop[i], (int)g.M, (int)g.K, 1});
-        else d.push_back(TnDesc{g.x, g.u, at(ws, off), g.dA, (int)g.M, (int)g.K, r, 1});
-        off += align256(tn_ws_bytes(g.M, g.K, r));
-        if (drops) dd.push_back(GradDropDesc{g.dy, g.t, at(ws, off), g.dB, DropArgs{}, (int)g.M, (int)g.N, 0});
-        else d.push_back(TnDesc{g.dy, g.t, at(ws, off), g.dB, (int)g.M, (int)g.N, 1, g.N});
-        off += align256(tn_ws_bytes(g.M, g.N, r));
+        if (g.M != 0) continue;  // empty sums
+        if ((st = launch_fill(g.dA, g.K * r, 0.0f, s)) != QLORA_OK) return st;
+        if ((st = launch_fill(g.dB, (int64_t)r * g.N, 0.0f, s)) != QLORA_OK) return st;
     }
-    if (!dd.empty() && (st = launch_grads_dropout(dd.data(), (int)dd.size(), r, dt_of(dtype), s)) != QLORA_OK) return st;
-    return launch_tn_batch(d.data(), (int)d.size(), r, dt_of(dtype), s);
+    // Layers that drop something first, then the others (the call without dropout, bit for bit): whole
+    // launches of each, gathered in fixed arrays.
+    for (int dropping = drops ? 1 : 0; dropping >= 0; --dropping) {
+        TnDesc d[kContractions];
+        GradDropDesc dd[kContractions];
+        int n = 0;
+        size_t off = 0;
+        for (int i = 0; i <= count; ++i) {
+            if (n == kContractions || (i == count && n)) {
+                st = dropping ? launch_grads_dropout(dd, n, r, dt_of(dtype), s) : launch_tn_batch(d, n, r, dt_of(dtype), s);
+                if (st != QLORA_OK) return st;
+                n = 0;
+            }
+            if (i == count || layers[i].M == 0) continue;
+            const qlora_lora_grads& g = layers[i];
+            const DropArgs drop = drop_of(drops, i);
+            uint8_t *const wa = at(ws, off), *const wb = wa + align256(tn_ws_bytes(g.M, g.K, r));
+            off += grads_ws(g, r);
+            if ((drop.thr != 0) != (dropping != 0)) continue;
+            // dA [K, r] = x^T u ; dB [r, N] = t^T dy, stored transposed from the [N, r] reduction
+            if (dropping) {
+                dd[n++] = GradDropDesc{g.x, g.u, wa, g.dA, drop, (int)g.M, (int)g.K, 1};
+                dd[n++] = GradDropDesc{g.dy, g.t, wb, g.dB, DropArgs{}, (int)g.M, (int)g.N, 0};
+            } else {
+                d[n++] = TnDesc{g.x, g.u, wa, g.dA, (int)g.M, (int)g.K, r, 1};
+                d[n++] = TnDesc{g.dy, g.t, wb, g.dB, (int)g.M, (int)g.N, 1, g.N};
+            }
+        }
+    }
+    return QLORA_OK;
 }
 
 qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, int r, int dtype, void* ws,
@@ -505,11 +532,8 @@ qlora_status qlora_lora_grads_batch(const qlora_lora_grads* layers, int count, i
 
 qlora_status qlora_lora_grads_batch_dropout(const qlora_lora_grads* layers, const qlora_dropout* drops, int count,
                                             int r, int dtype, void* ws, size_t ws_bytes, void* stream) {
-    if (count <= 0) return lora_grads_batch(layers, nullptr, count, r, dtype, ws, ws_bytes, stream);
-    std::vector<DropArgs> d;
-    bool any;
-    if (!drops || !drops_of(drops, count, d, any)) return QLORA_ERR_INVALID_ARG;
-    return lora_grads_batch(layers, any ? d.data() : nullptr, count, r, dtype, ws, ws_bytes, stream);
+    if (count > 0 && (!drops || !good_drops(drops, count))) return QLORA_ERR_INVALID_ARG;
+    return lora_grads_batch(layers, drops, count, r, dtype, ws, ws_bytes, stream);
 }
 
 qlora_status qlora_linear_fwd(const qlora_nf4* w, const uint16_t* x, int64_t M, const uint16_t* A, const uint16_t* B,

@@ -109,7 +109,7 @@ __device__ __forceinline__ void drop_tile_rows(f32x16_t& f, const DropArgs& d, u
 // multiples of 2^-16 too).  A null d drops nothing.
 bool drop_args(const qlora_dropout* d, DropArgs* out);
 
-// launch_nt_batch (Y natural) with drop[i] on X of product i
+// launch_nt_batch (Y natural) with drop[i] (thr > 0) on X of product i
 qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s);
 // The gradients of layers that drop something: dA = drop(X)^T S into out [D, r], or (dA 0) dB = S^T X into
 // out [r, D]; D below kGradMaxWidth.  ws: tn_ws_bytes(M, D, r) bytes that need no clearing.

@@ -1,7 +1,6 @@
 // The LoRA branch's product with dropout (dropout.h), t = s drop(x) A of several layers in one launch
 // (lora_prep.h), and the generator's arguments.
 #include <cmath>
-#include <vector>
 
 #include "lora_prep.h"
 
@@ -67,21 +66,9 @@ qlora_status down_stream(const NtDesc* d, const DropArgs* drop, int n, int r, in
 }  // namespace
 
 qlora_status launch_nt_batch_dropout(const NtDesc* d, const DropArgs* drop, int count, int r, int dt, hipStream_t s) {
-    std::vector<NtDesc> plain, rest;   // (nothing dropped: the product of the call without dropout, bit for bit)
-    std::vector<DropArgs> rest_drop;
-    for (int i = 0; i < count; ++i) {
-        if (!drop[i].thr) {
-            plain.push_back(d[i]);
-            continue;
-        }
-        rest.push_back(d[i]);
-        rest_drop.push_back(drop[i]);
-    }
     qlora_status st = QLORA_OK;
-    if (!plain.empty()) st = launch_nt_batch(plain.data(), (int)plain.size(), true, r, dt, s);
-    for (size_t i = 0; i < rest.size() && st == QLORA_OK; i += kStreamItems)
-        st = down_stream(rest.data() + i, rest_drop.data() + i, (int)std::min<size_t>(kStreamItems, rest.size() - i), r, dt,
-                         s);
+    for (int i = 0; i < count && st == QLORA_OK; i += kStreamItems)
+        st = down_stream(d + i, drop + i, std::min(kStreamItems, count - i), r, dt, s);
     return st;
 }
 

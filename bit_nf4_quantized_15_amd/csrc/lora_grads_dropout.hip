@@ -22,7 +22,6 @@
 // without dropout go, took 189 us.)  One layer of 500 tokens, 4096 -> 11008, r = 16: 11.4 us (15.4), a
 // tile's latency.
 #include <cstring>
-#include <vector>
 
 #include "dropout.h"
 #include "grads_plan.h"
