@@ -49,6 +49,14 @@ struct StreamArgs {
     int n, r;
 };
 
+// What lanes of a wave read from LDS that is the wave's own comes after what its other lanes wrote
+// there.  No instruction: a wave's LDS accesses are done in order, and the compiler keeps to it.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // TQ: groups of 32 ranks.  VEC: rows of X and Y are whole 16-byte chunks.  DROP: thr > 0.
 template <int TQ, bool VEC, bool YNAT, bool DROP, bool QUANT, int DT>
 __device__ __forceinline__ void stream_body(const StreamArgs& args) {
@@ -127,34 +135,51 @@ __device__ __forceinline__ void stream_body(const StreamArgs& args) {
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
             u32x4_t v = __builtin_bit_cast(u32x4_t, q.x[p]);
+            if constexpr (DROP) v = drop8(v, a.drop, (uint32_t)(c0 + ch8) >> 3, (uint32_t)(row0 + 4 * p));
+            *reinterpret_cast<u32x4_t*>(&xw[((lane >> 4) + 4 * p) * kLdX + ch8]) = v;
+        }
+        auto read_y = [&](int i, int t) __attribute__((always_inline)) {   // columns 16 i + 8 h .. of ranks 32 t ..
+            const int c = 16 * i + 8 * h;
+            return YNAT ? slice_col8(ys[buf], kLdN, c, 32 * t + 16 * tg, tj)
+                        : *reinterpret_cast<const bf16x8*>(&ys[buf][(32 * t + l32) * kLdT + c]);
+        };
+        bf16x8 y[2][TQ], xo[2];   // operands: 16 columns' are read while the 16 before are multiplied
+#pragma unroll
+        for (int t = 0; t < TQ; ++t) y[0][t] = read_y(0, t);
+        // No memory access moves across the order point: the codes are stored behind it, beside the
+        // products, and Y's first operands are read in front.  (With the codes in front, and operands
+        // read as they are used, it cost up to 4 %, r = 128.)  What lanes read for block b - 1 lies
+        // behind the barrier before this block.
+        wave_lds_order();
+        auto read_x = [&](int i) __attribute__((always_inline)) {
+            return *reinterpret_cast<const bf16x8*>(&xw[l32 * kLdX + 16 * i + 8 * h]);
+        };
+        xo[0] = read_x(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i < 7) {
+                xo[(i + 1) & 1] = read_x(i + 1);
+#pragma unroll
+                for (int t = 0; t < TQ; ++t) y[(i + 1) & 1][t] = read_y(i + 1, t);
+            }
             if constexpr (QUANT) {
+                const u32x4_t v = __builtin_bit_cast(u32x4_t, q.x[i]);
                 uint32_t top = 0;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) top = max_mag2(top, v[w]);
                 const uint32_t byte = fp8_scale_byte<DT>(max_row16(top));
-                mine = (lane & 7) == p ? byte : mine;
+                mine = (lane & 7) == i ? byte : mine;
                 // (rows past M lie past the buffer and are dropped)
                 __builtin_amdgcn_raw_buffer_store_b64(fp8_codes8<DT>(v, byte), qrs,
-                                                      to + 4u * (uint32_t)p * (uint32_t)args.q.ld, 0, 0);
+                                                      to + 4u * (uint32_t)i * (uint32_t)args.q.ld, 0, 0);
             }
-            if constexpr (DROP) v = drop8(v, a.drop, (uint32_t)(c0 + ch8) >> 3, (uint32_t)(row0 + 4 * p));
-            *reinterpret_cast<u32x4_t*>(&xw[((lane >> 4) + 4 * p) * kLdX + ch8]) = v;
+#pragma unroll
+            for (int t = 0; t < TQ; ++t) acc[t] = mfma32<DT>(xo[i & 1], y[i & 1][t], acc[t]);
         }
         if constexpr (QUANT) {
             const int row = row0 + 4 * (lane & 7);
             const rsrc_t srs = buf_rsrc(args.q.scale + (int64_t)(c0 >> 7) * args.q.rs + bm0, (uint64_t)min(128, M - bm0));
             __builtin_amdgcn_raw_buffer_store_b8((uint8_t)mine, srs, (lane & 15) < 8 ? (uint32_t)(row - bm0) : kNone, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = 16 * i + 8 * h;   // columns of the lane's k slots
-            const bf16x8 x = *reinterpret_cast<const bf16x8*>(&xw[l32 * kLdX + c]);
-#pragma unroll
-            for (int t = 0; t < TQ; ++t) {
-                const bf16x8 y = YNAT ? slice_col8(ys[buf], kLdN, c, 32 * t + 16 * tg, tj)
-                                      : *reinterpret_cast<const bf16x8*>(&ys[buf][(32 * t + l32) * kLdT + c]);
-                acc[t] = mfma32<DT>(x, y, acc[t]);
-            }
         }
     };
     Cols q0, q1;
