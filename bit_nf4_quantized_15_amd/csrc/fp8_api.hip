@@ -26,6 +26,9 @@ inline int64_t scale_stride(int64_t rows, int64_t cols, int block_rows) {
     return pad4(block_rows == 1 ? rows : fp8_blocks(cols));
 }
 
+// Elements of a tensor that the codes are made of, or restored to: 16 a thread of a grid.
+constexpr int64_t kMaxElements = int64_t(1) << 36;
+
 // A weight (min_rows 1) or activations (min_rows 0, where an empty one needs no pointers).
 qlora_status check_fp8(const qlora_fp8* q, int64_t min_rows) {
     if (!q || q->rows < min_rows || q->cols < 1 || !is16(q->dtype)) return QLORA_ERR_INVALID_ARG;
@@ -82,6 +85,7 @@ qlora_status qlora_fp8_quantize(const uint16_t* x, const qlora_fp8* out, void* s
     const qlora_status st = check_fp8(out, 0);
     if (st != QLORA_OK) return st;
     if (out->rows == 0) return QLORA_OK;
+    if (out->rows * out->cols >= kMaxElements) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (!x) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(x)) return QLORA_ERR_MISALIGNED;
     const int64_t rs = scale_stride(out->rows, out->cols, out->block_rows);
@@ -96,6 +100,7 @@ qlora_status qlora_fp8_dequantize(const qlora_fp8* q, uint16_t* out, void* strea
     const qlora_status st = check_fp8(q, 0);
     if (st != QLORA_OK) return st;
     if (q->rows == 0) return QLORA_OK;
+    if (q->rows * q->cols >= kMaxElements) return QLORA_ERR_UNSUPPORTED_SHAPE;
     if (!out) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(out)) return QLORA_ERR_MISALIGNED;
     return launch_fp8_dequantize(q->codes, q->scale, q->rows, q->cols, scale_stride(q->rows, q->cols, q->block_rows),
