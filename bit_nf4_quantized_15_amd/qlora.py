@@ -221,7 +221,8 @@ def _dev(t, dtype, name, shape=None):
 class Dropout:
     """Dropout of a LoRA branch's input (struct qlora_dropout): probability p, and the counter-based generator's seed
     and offset, 64 bits each.  The forward and the backward of a layer are given the same one; layers and steps whose
-    masks are to differ take other offsets or seeds.  p acts as round(65536 p) / 65536."""
+    masks are to differ take other offsets or seeds.  Seed and offset are read when a call is made: one captured into
+    a graph has the same mask at every replay.  p acts as round(65536 p) / 65536."""
 
     def __init__(self, p, seed=0, offset=0):
         if not 0.0 <= p < 1.0 or round(p * 65536) > 65535:

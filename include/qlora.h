@@ -480,6 +480,10 @@ qlora_status qlora_lora_grads_batch_int8(const qlora_lora_grads_int8* layers, in
  * where these 16 bits are at least P = round(65536 p) (ties to even), and 1 - p above
  * stands for 1 - P / 65536.  Layers and steps that must not share a mask take other
  * offsets or seeds; a mask depends on neither M, N, K nor r.
+ * seed and offset are read when a call is made and go to its kernels by value: a call that
+ * was captured into a HIP graph has the same mask at every replay.  A captured step whose
+ * masks are to change from replay to replay is captured again with another offset, or
+ * leaves the calls that take a drop outside the graph.
  * A dropped value counts as zero, whatever it is.  The factor 1 / (1 - p) is applied to
  * fp32 sums: no 16-bit value is rounded for it.
  * 0 <= p < 1 and P <= 65535, otherwise INVALID_ARG; P = 0 is the call without dropout,
