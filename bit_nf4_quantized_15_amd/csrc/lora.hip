@@ -98,6 +98,61 @@ __global__ void fill_f32_kernel(float* __restrict__ out, int64_t count, float v)
     if (i < count) out[i] = v;
 }
 
+// Grid and arguments of a launch over the n <= kNtBatch products d.  vec: the conditions of
+// launch_nt's vector path, for every product of the launch.
+qlora_status nt_batch(const NtDesc* d, int n, bool y_natural, int r, NtBatch& b, bool& vec, int& chunk,
+                      unsigned& total) {
+    b.n = n;
+    b.r = r;
+    vec = !y_natural || r % 8 == 0;
+    int64_t sum = 0;
+    for (int i = 0; i < n; ++i) {
+        const NtDesc& e = d[i];
+        const SplitPlan sp = plan_nt(e.M, e.C, r);
+        NtProb& p = b.p[i];
+        p.X = e.X;
+        p.Y = e.Y;
+        p.tiles = (e.M + 127) / 128;
+        p.splits = sp.splits;
+        p.chunk = sp.chunk;
+        p.tags = static_cast<uint64_t*>(e.ws);
+        p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(e.ws) + split_tags_bytes(p.tiles, sp));
+        p.out = e.out;
+        p.scale = e.scale;
+        p.M = e.M;
+        p.C = e.C;
+        vec = vec && (e.C % 8 == 0) && ((reinterpret_cast<uintptr_t>(e.X) & 15u) == 0) &&
+              ((reinterpret_cast<uintptr_t>(e.Y) & 15u) == 0) && (int64_t)e.C * 128 * 2 < (int64_t(1) << 30);
+        chunk = std::max(chunk, sp.chunk);
+        b.first[i] = (int)sum;
+        sum += (int64_t)p.tiles * p.splits;
+        if (sum >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    }
+    b.first[n] = (int)sum;
+    total = (unsigned)sum;
+    return QLORA_OK;
+}
+
+// The same over the n <= kTnBatch contractions d.
+qlora_status tn_batch(const TnDesc* d, int n, int r, TnBatch& b, bool& vec, int& chunk, unsigned& total) {
+    b.n = n;
+    vec = true;
+    int64_t sum = 0;
+    for (int i = 0; i < n; ++i) {
+        const TnDesc& e = d[i];
+        bool v = false;
+        b.p[i] = tn_prob(e.X, e.S, e.ws, e.out, e.M, e.D, r, e.ld_d, e.ld_j, v);
+        vec = vec && v;
+        chunk = std::max(chunk, b.p[i].chunk);
+        b.first[i] = (int)sum;
+        sum += (int64_t)b.p[i].tiles * b.p[i].splits;
+        if (sum >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    }
+    b.first[n] = (int)sum;
+    total = (unsigned)sum;
+    return QLORA_OK;
+}
+
 inline unsigned blocks_for(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 
 }  // namespace
