@@ -23,11 +23,11 @@
 //
 // Bound by the MFMAs and the power they draw (from registers alone the chip reaches 4.0 PFLOP/s).
 // 8192 x 28672 x 8192, us: 1285 to 1360 for given codes, r = 0 (3.0 PFLOP/s; a library product of
-// these sizes without the blocks' scales 1331), 1600 to 1680 traced with the LoRA term behind the
-// preparation.  Input gradient 4096 x 11008 -> 4096, r = 64, dropout 0.05, traced: 151, one round of 256
-// tiles (2.5 PFLOP/s), of which the epilogue's masks are 5.  Ragged: 333 x 11008 -> 4096, r = 8: 29
-// (split in two); input gradient 777 x 11000 -> 4096, r = 24: 48 (224 of 256 CUs).
-// The 256 x 256 input gradient with dropout keeps up to 280 bytes a lane in scratch memory while its
+// these sizes without the blocks' scales 1331), 1570 to 1640 traced with the LoRA term behind the
+// preparation.  Input gradient 4096 x 11008 -> 4096, r = 64, dropout 0.05, traced: 150, one round of 256
+// tiles (2.5 PFLOP/s), of which the epilogue's masks are 5.  Ragged: 333 x 11008 -> 4096, r = 8: 28
+// (split in two); input gradient 777 x 11000 -> 4096, r = 24: 46 (224 of 256 CUs).
+// The 256 x 256 input gradient with dropout keeps 260 bytes a lane in scratch memory while its
 // epilogue makes masks: outside the main loop, and less than a second pass over the tile would cost.
 #include <algorithm>
 

@@ -11,9 +11,9 @@
 // workgroup of the last range as lora_body.h does, left that to one CU per 128 tokens: 333 x
 // 11008, r = 8 took 24 us, 4096 x 11008, r = 64 38 us.)
 //
-// Traced, us, the pass and the second kernel: x 8192 x 8192, r = 64, dropout, with codes 56 + 7 (HBM: 4.0
+// Traced, us, the pass and the second kernel: x 8192 x 8192, r = 64, dropout, with codes 50 + 7 (HBM: 4.0
 // TB/s in the pass); dy 4096 x 11008, r = 64, with codes 32 + 5; x 333 x 11008, r = 8, dropout, with
-// codes 8.8 + 4.4, latencies; t of three layers that share x 4096 x 4096, r = 64, dropout, 25 + 7:
+// codes 7.9 + 4.7, latencies; t of three layers that share x 4096 x 4096, r = 64, dropout, 24 + 7:
 // the generator's 12 us of every SIMD's time in the pass, whose x comes from the caches twice.
 #pragma once
 
