@@ -10,8 +10,6 @@ import pytest
 
 from bit_nf4_quantized_15_amd import build
 
-from test_isa_waits import _kernels
-
 pytestmark = pytest.mark.skipif(not os.path.exists(build.HIPCC) and shutil.which("hipcc") is None,
                                 reason="hipcc not available")
 SOURCES = {"fp8_prep": ("fp8_prep_stream_kernelI", 48), "lora_dropout": ("down_stream_kernelI", 16)}
@@ -33,6 +31,13 @@ def asm(tmp_path_factory):
     return out
 
 
+def kernels(asm, pattern):
+    """(name, lines) of each kernel whose name holds the pattern."""
+    for m in re.finditer(r"^(_Z\w+):\s*(?:;.*)?$", asm, re.M):
+        if pattern in m.group(1):
+            yield m.group(1), [l.strip() for l in asm[m.start():asm.find(".Lfunc_end", m.start())].split("\n")]
+
+
 def args(name):
     """Groups of 32 ranks, and whether Y is [C, r]."""
     v = [int(v) for v in re.findall(r"L[ibj](\d+)E", name.split("_kernelI", 1)[1])]
@@ -43,7 +48,7 @@ def args(name):
 def test_reads_of_other_lanes_values_follow_the_order_point(asm, source):
     pattern, count = SOURCES[source]
     n = 0
-    for name, body in _kernels(asm[source], pattern):
+    for name, body in kernels(asm[source], pattern):
         points = [i for i, l in enumerate(body) if l.startswith("; wave barrier")]
         assert len(points) == 2, (name, len(points))                      # the two blocks of a turn
         groups, ynat = args(name)
